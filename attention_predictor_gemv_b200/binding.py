@@ -24,8 +24,9 @@ DV_OK, DV_ERR_ARG, DV_ERR_ALIGN, DV_ERR_UNSUPPORTED, DV_ERR_CUDA, DV_ERR_DEVICE,
 DV_F32, DV_BF16 = 0, 1
 DV_TOPK, DV_THRESHOLD = 0, 1
 DV_ACT_RELU, DV_ACT_GELU = 0, 1
-(DV_OP_PREDICT_MLP, DV_OP_PREDICT_HEADS, DV_OP_TOPK, DV_OP_SPARSE_MLP, DV_OP_SPARSE_MHA,
- DV_OP_DECODE_LAYER) = range(6)
+(DV_OP_PREDICT_MLP, DV_OP_PREDICT_HEADS, DV_OP_TOPK, DV_OP_SPARSE_MLP, DV_OP_SPARSE_MHA, DV_OP_DECODE_LAYER,
+ DV_OP_PAGE_TABLES, DV_OP_PAGED_APPEND, DV_OP_PAGED_ATTN, DV_OP_SPARSE_MHA_PAGED) = range(10)
+DV_DEV_COUNT_CLAMPED, DV_DEV_INDEX_RANGE, DV_DEV_BAD_PARTIAL, DV_DEV_TIMEOUT, DV_DEV_REFUSED = 1, 2, 4, 8, 16
 
 
 class DvError(RuntimeError):
@@ -59,6 +60,11 @@ class LayerParamsC(ctypes.Structure):
 class LayerIOC(ctypes.Structure):
     _fields_ = [("yA", _p), ("scores_h", _p), ("head_idx", _p), ("head_count", _p), ("yM", _p), ("scores", _p),
                 ("idx", _p), ("count", _p)]
+
+
+class PagedKVC(ctypes.Structure):
+    _fields_ = [("kvdtype", _c_int), ("K", _p), ("V", _p), ("page_stride", ctypes.c_longlong), ("n_pages", _c_int),
+                ("page", _c_int), ("h_kv", _c_int), ("dh", _c_int)]
 
 
 def _sig(name, res, args):
@@ -125,6 +131,17 @@ _lib_dv_topk_static = _sig("dv_topk_static", _c_int, [_p, _c_int, _c_int, _c_int
 _lib_dv_prefetch_layer = _sig("dv_prefetch_layer", _c_int,
                               [ctypes.POINTER(LayerWeightsC), ctypes.POINTER(Dims), ctypes.POINTER(LayerIOC), _c_int,
                                _c_int, _p])
+_lib_dv_page_tables = _sig("dv_page_tables", _c_int,
+                           [_p, _c_int, _c_int, _c_int, _c_int, _p, _p, _p, _p, _p, _p, _c_int, _p, _p, _p, _p, _c_size,
+                            _p])
+_lib_dv_paged_append = _sig("dv_paged_append", _c_int,
+                            [ctypes.POINTER(PagedKVC), _p, _p, _c_int, _p, _p, _c_size, _p])
+_lib_dv_paged_attn = _sig("dv_paged_attn", _c_int,
+                          [ctypes.POINTER(PagedKVC), _p, _c_int, _c_int, _p, _c_int, _p, _c_float, _p, _p, _c_int, _p,
+                           _p, _p, _c_size, _p])
+_lib_dv_sparse_mha_paged = _sig("dv_sparse_mha_paged", _c_int,
+                                [_p, _c_int, _c_int, _p, _p, _p, _p, _c_int, ctypes.POINTER(PagedKVC), _p, _c_int, _p,
+                                 _p, _c_float, _p, _p, _c_int, _p, _c_int, _c_int, _p, _c_size, _p])
 _lib_dv_launch_count = _sig("dv_launch_count", ctypes.c_uint64, [])
 
 
@@ -421,3 +438,125 @@ def dv_predict_layer_tail(layer: Layer, p: LayerParamsC, out: LayerIOC, ws, sets
 def dv_prefetch_layer(layer: Layer, sel: LayerIOC, pos, with_w2=True, stream=None):
     _check(_lib_dv_prefetch_layer(ctypes.byref(layer.c), ctypes.byref(layer.dims), ctypes.byref(sel), int(pos),
                                   int(bool(with_w2)), _stream(stream)), "dv_prefetch_layer")
+
+
+# ---------------------------------------------------------------------------
+# paged key-value cache
+# ---------------------------------------------------------------------------
+
+
+class PagedKV:
+    """The pools K, V [n_pages][h_kv][page][dh] (bf16 or fp32) of a paged
+    cache, marshalled into the dv_paged_kv struct and kept alive. Each page
+    must be contiguous; pages may lie further apart (a view of a pool that
+    several layers, or K and V, share), at the same distance in K and V."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor):
+        if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or K.device != V.device:
+            raise ValueError(f"K and V must be alike, [n_pages][h_kv][page][dh]: got {tuple(K.shape)} {K.dtype} on "
+                             f"{K.device} and {tuple(V.shape)} {V.dtype} on {V.device}")
+        n_pages, h_kv, page, dh = K.shape
+        if K.numel() == 0:
+            raise ValueError(f"an empty pool: {tuple(K.shape)}")
+        for n, t in (("K", K), ("V", V)):
+            if not t[0].is_contiguous() or (n_pages > 1 and t.stride(0) < h_kv * page * dh):
+                raise ValueError(f"{n}: the elements of a page must be contiguous, strides {t.stride()}")
+            if not t.is_cuda:
+                raise ValueError(f"{n} must be a CUDA tensor")
+        if n_pages > 1 and K.stride(0) != V.stride(0):
+            raise ValueError(f"K and V pages lie at different distances: {K.stride(0)} and {V.stride(0)}")
+        self.K, self.V, self.device = K, V, K.device
+        self.n_pages, self.h_kv, self.page, self.dh = n_pages, h_kv, page, dh
+        self.c = PagedKVC(_wdt(K), K.data_ptr(), V.data_ptr(), K.stride(0) if n_pages > 1 else 0, n_pages, page, h_kv, dh)
+        self.ref = ctypes.byref(self.c)
+
+
+def _arg(t: Optional[torch.Tensor], dtype, shape, device, name: str) -> Optional[int]:
+    """Pointer of a contiguous tensor of this dtype, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}; expected {shape} "
+                         f"{dtype} on {device}, contiguous")
+    return t.data_ptr()
+
+
+def _ws_arg(ws: torch.Tensor, device) -> int:
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: {ws.dtype} on {ws.device}; expected a workspace on {device}")
+    return ws.data_ptr()
+
+
+def _launch(fn, name: str, device, stream, *args):
+    """fn(*args, stream) on the tensors' own device: its current stream unless one is given."""
+    if not device.type == "cuda":
+        raise ValueError(f"{name}: CUDA tensors are needed, got {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{name}: a stream of {stream.device} for tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        s = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            s = fn(*args, _stream(stream))
+    _check(s, name)
+
+
+def dv_page_tables(want, lens, lens_out, table, free_list, free_count, free_count_out, slots, offsets, granted, page, ws,
+                   stream=None):
+    """Block tables [R][W], slots and the free stack from the requests'
+    current and wanted lengths (int32, on the device)."""
+    dev, i32 = want.device, torch.int32
+    R, W = table.shape
+    n_pages, max_tokens = free_list.shape[0], slots.shape[0]
+    _launch(_lib_dv_page_tables, "dv_page_tables", dev, stream, _arg(want, i32, (R,), dev, "want"), R, int(page), n_pages, W,
+            _arg(lens, i32, (R,), dev, "lens"), _arg(lens_out, i32, (R,), dev, "lens_out"),
+            _arg(table, i32, (R, W), dev, "table"), _arg(free_list, i32, (n_pages,), dev, "free_list"),
+            _arg(free_count, i32, (1,), dev, "free_count"), _arg(free_count_out, i32, (1,), dev, "free_count_out"),
+            max_tokens, _arg(slots, i32, (max_tokens,), dev, "slots"), _arg(offsets, i32, (R + 1,), dev, "offsets"),
+            _arg(granted, i32, (R,), dev, "granted"), _ws_arg(ws, dev), ws.numel())
+
+
+def dv_paged_append(kv: PagedKV, k, v, slots, ws, stream=None):
+    """k, v [T][h_kv][dh] fp32 of new tokens into their slots [T] of the pools."""
+    dev, T = kv.device, slots.shape[0]
+    shape = (T, kv.h_kv, kv.dh)
+    if T == 0:
+        return
+    _launch(_lib_dv_paged_append, "dv_paged_append", dev, stream, kv.ref, _arg(k, torch.float32, shape, dev, "k"),
+            _arg(v, torch.float32, shape, dev, "v"), T, _arg(slots, torch.int32, (T,), dev, "slots"), _ws_arg(ws, dev),
+            ws.numel())
+
+
+def dv_paged_attn(q, kv: PagedKV, table, lens, scale, out, ws, lse=None, head_idx=None, head_count=None, stream=None):
+    """Attention of one new token per request over its pages. q, out
+    [B][h_q][dh]; with a set head_idx / head_count of key-value heads they are
+    [B][kh_max * G][dh], G query heads for each place of the set, kh_max =
+    len(head_idx), and h_q = G * h_kv."""
+    dev, i32, f32 = kv.device, torch.int32, torch.float32
+    B, rows, dh = q.shape
+    heads = kv.h_kv if head_idx is None else head_idx.shape[0]
+    if head_idx is not None and head_count is None or heads == 0 or rows % heads != 0 or dh != kv.dh:
+        raise ValueError(f"q: {tuple(q.shape)} for {heads} key-value heads of {kv.dh} channels")
+    W = table.shape[1]
+    _launch(_lib_dv_paged_attn, "dv_paged_attn", dev, stream, kv.ref, _arg(q, f32, (B, rows, dh), dev, "q"), B,
+            rows // heads * kv.h_kv, _arg(table, i32, (B, W), dev, "table"), W, _arg(lens, i32, (B,), dev, "lens"),
+            float(scale), _arg(head_idx, i32, (heads,), dev, "head_idx"), _arg(head_count, i32, (1,), dev, "head_count"),
+            heads if head_idx is not None else 0, _arg(out, f32, (B, rows, dh), dev, "out"),
+            _arg(lse, f32, (B, rows), dev, "lse"), _ws_arg(ws, dev), ws.numel())
+
+
+def dv_sparse_mha_paged(y, Wqkv, bqkv, WOt, bO, kv: PagedKV, table, lens, slots, scale, head_idx, head_count, kh_max, out,
+                        ws, accumulate=False, exact_kv=False, stream=None):
+    """dv_sparse_mha over a paged cache: per-row lengths [B], the new token's slot [B]."""
+    dev, i32, f32 = kv.device, torch.int32, torch.float32
+    B, d = y.shape
+    h, dh, W = kv.h_kv, kv.dh, table.shape[1]
+    if head_idx.shape[0] < kh_max:
+        raise ValueError(f"head_idx has {head_idx.shape[0]} entries, kh_max is {kh_max}")
+    _launch(_lib_dv_sparse_mha_paged, "dv_sparse_mha_paged", dev, stream, _arg(y, f32, (B, d), dev, "y"), B, d,
+            _arg(Wqkv, Wqkv.dtype, (h, 3, dh, d), dev, "Wqkv"), _arg(bqkv, f32, (h, 3, dh), dev, "bqkv"),
+            _arg(WOt, Wqkv.dtype, (h, dh, d), dev, "WOt"), _arg(bO, f32, (d,), dev, "bO"), _wdt(Wqkv), kv.ref,
+            _arg(table, i32, (B, W), dev, "table"), W, _arg(lens, i32, (B,), dev, "lens"),
+            _arg(slots, i32, (B,), dev, "slots"), float(scale), _arg(head_idx, i32, tuple(head_idx.shape), dev, "head_idx"),
+            _arg(head_count, i32, (1,), dev, "head_count"), int(kh_max), _arg(out, f32, (B, d), dev, "out"),
+            int(bool(accumulate)), int(bool(exact_kv)), _ws_arg(ws, dev), ws.numel())

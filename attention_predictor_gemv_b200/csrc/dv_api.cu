@@ -9,6 +9,7 @@
 #include "../../include/dejavu.h"
 #include "dv_api_kernels.cuh"
 #include "dv_launchers.cuh"
+#include "dv_paged_launch.h"
 #include "dv_tc_launch.h"
 
 using namespace dv;
@@ -22,7 +23,7 @@ constexpr int ATTN_S_MIN = 32;
 // calls of different operations may share one workspace: the status word at
 // 0, the selection tickets at 16, 32, 48 and 64, and the attention split
 // counters [B][kh_max] from 1024.
-constexpr size_t WS_HEADER = 72 * 1024;
+// (WS_HEADER and the counters' offset: dv_paged_launch.h)
 constexpr int KH_LIMIT = 1000;  // B * kh_max counters must fit the header
 
 // Workspace layout. Offsets in bytes from the workspace base.
@@ -53,7 +54,7 @@ Layout layout(const dv_dims& D, int wbytes) {
   L.sel_ticket_m = L.status + 32;
   L.pa_ticket = L.status + 48;
   L.pb_ticket = L.status + 64;
-  L.attn_ctr = L.status + 1024;
+  L.attn_ctr = L.status + WS_TICKETS;
   L.t1 = take(4ull * B * D.d);
   L.yA = take(4ull * B * D.d);
   L.yM = take(4ull * B * D.d);
@@ -293,6 +294,24 @@ int wbytes_of(dv_dtype t) { return t == DV_BF16 ? 2 : 4; }
 bool dtype_ok(int t) { return t == DV_F32 || t == DV_BF16; }
 bool mode_ok(int m) { return m == DV_TOPK || m == DV_THRESHOLD; }
 bool act_ok(int a) { return a == DV_ACT_RELU || a == DV_ACT_GELU; }
+
+// Workspace of dv_sparse_mha_paged: the layout of its projections, then the
+// new token's k and v rows [B][h][dh] and the attention's partials.
+struct PagedLayout {
+  Layout L;
+  size_t ks, vs, part, total;
+};
+
+PagedLayout paged_layout(const dv_dims& D, int wbytes) {
+  PagedLayout P = {};
+  P.L = layout(D, wbytes);
+  const size_t rows = up256((size_t)D.B * D.h * D.dh * wbytes);
+  P.ks = P.L.total;
+  P.vs = P.ks + rows;
+  P.part = P.vs + rows;
+  P.total = P.part + 4 * paged_attn_part_floats(D.dh);
+  return P;
+}
 
 dv_status check_ws(const Layout& L, void* ws, size_t ws_bytes) {
   if (!ok_ptr(ws)) return ws ? DV_ERR_ALIGN : DV_ERR_ARG;
@@ -817,8 +836,19 @@ const char* dv_status_string(dv_status s) {
 }
 
 size_t dv_workspace_size(int op, const dv_dims* dims) {
-  if (!dims || op < DV_OP_PREDICT_MLP || op > DV_OP_DECODE_LAYER) return 0;
+  if (!dims || op < DV_OP_PREDICT_MLP || op > DV_OP_SPARSE_MHA_PAGED) return 0;
   dv_dims D = *dims;
+  if (op == DV_OP_PAGE_TABLES || op == DV_OP_PAGED_APPEND) return WS_HEADER;
+  if (op == DV_OP_PAGED_ATTN)
+    return D.dh < 8 || D.dh % 8 != 0 || D.dh > PAGED_MAX_DH ? 0 : WS_HEADER + 4 * paged_attn_part_floats(D.dh);
+  if (op == DV_OP_SPARSE_MHA_PAGED) {
+    D.N = 1;
+    D.r = D.cap = D.k_max = 0;
+    if (!dims_ok(D) || (D.dh != 64 && D.dh != 128) || D.h < 1) return 0;
+    size_t n = 0;
+    for (int wb : {2, 4}) n = paged_layout(D, wb).total > n ? paged_layout(D, wb).total : n;
+    return n;
+  }
   if (op == DV_OP_TOPK) {
     D.d = 8;
     D.r = 0;
@@ -921,6 +951,56 @@ dv_status dv_sparse_mha(const float* y, int B, int d, int h, int dh, const void*
   DV_CHECK(check_ws(L, ws, ws_bytes));
   return do_sparse_mha(L, ws, y, B, d, h, dh, Wqkv, bqkv, WOt, bO, wdtype, Kc, Vc, cap, pos, scale, head_idx,
                        head_count, kh_max, out, accumulate, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, const float* bqkv, const void* WOt,
+                              const float* bO, dv_dtype wdtype, const dv_paged_kv* kv, const int32_t* table, int W,
+                              const int32_t* lens, const int32_t* slots, float scale, const int32_t* head_idx,
+                              const int32_t* head_count, int kh_max, float* out, int accumulate, int exact_kv, void* ws,
+                              size_t ws_bytes, dv_stream_t stream) {
+  DV_CHECK(paged_kv_check(kv));
+  if (!dtype_ok(wdtype)) return DV_ERR_ARG;
+  if (kv->kvdtype != wdtype) return DV_ERR_UNSUPPORTED;
+  if (!y || !Wqkv || !WOt || !table || !lens || !slots || !head_idx || !head_count || !out || W < 1) return DV_ERR_ARG;
+  if (!ok_ptr(y) || !ok_ptr(Wqkv) || !ok_ptr(WOt) || !ok_ptr(table) || !ok_ptr(lens) || !ok_ptr(slots) ||
+      !ok_ptr(out) || !ok_opt(bO) || !ok_opt(bqkv) || !ok_ptr(head_idx) || !ok_ptr(head_count))
+    return DV_ERR_ALIGN;
+  const int h = kv->h_kv, dh = kv->dh;
+  if ((dh != 64 && dh != 128) || h > KV_REST_MAX_H) return DV_ERR_UNSUPPORTED;
+  dv_dims D = {B, d, 1, 0, h, dh, 0, 0, kh_max};
+  if (!dims_ok(D)) return DV_ERR_ARG;
+  if (kv->page > (INT32_MAX / 32) / W / B) return DV_ERR_UNSUPPORTED;
+  const PagedLayout P = paged_layout(D, wbytes_of(wdtype));
+  const Layout& L = P.L;
+  if (!ok_ptr(ws)) return ws ? DV_ERR_ALIGN : DV_ERR_ARG;
+  if (ws_bytes < P.total) return DV_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int* status = at<int>(ws, L.status);
+  float *q = at<float>(ws, L.q), *H = at<float>(ws, L.H);
+  void *ks = at<char>(ws, P.ks), *vs = at<char>(ws, P.vs);
+  // the projections store k and v as into a cache of one slot
+  const bool tc = tc_ok(B, d, wdtype, dh, 0);
+  if (kh_max > 0) {
+    if (tc)
+      DV_CHECK(tc_qkv(L, ws, y, B, d, h, dh, Wqkv, bqkv, ks, vs, 1, 0, head_idx, head_count, kh_max, st));
+    else
+      DV_TRY(run_qkv_dt(wdtype, Wqkv, d, h, dh, y, B, bqkv, head_idx, head_count, kh_max, q, ks, vs, 1, 0, status, st));
+  }
+  if (exact_kv)
+    DV_TRY(run_kv_rest_dt(wdtype, Wqkv, d, h, dh, y, B, bqkv, head_idx, head_count, kh_max, ks, vs, 1, 0, status, st));
+  DV_TRY(run_paged_token(kv, ks, vs, slots, B, head_idx, head_count, kh_max, exact_kv != 0, accumulate ? nullptr : out, d,
+                         status, st));
+  if (kh_max > 0)
+    DV_TRY(run_paged_attn(kv, q, B, kh_max, 1, table, W, lens, scale, head_idx, head_count, H, nullptr,
+                          at<float>(ws, P.part), at<unsigned>(ws, L.attn_ctr), status, st));
+  if (tc) return tc_wo(L, ws, B, d, h, dh, WOt, bO, head_idx, head_count, kh_max, out, st);
+  if (kh_max == 0) {
+    if (!bO) return DV_OK;
+    RowsHeads none{head_idx, head_count, nullptr, 0, dh, h};
+    return cuda_status(run_axpy_dt(wdtype, WOt, d, h * dh, none, bO, out, B, 1, 0, status, st));
+  }
+  RowsHeads src{head_idx, head_count, H, kh_max, dh, h};
+  return cuda_status(run_axpy_dt(wdtype, WOt, d, h * dh, src, bO, out, B, kh_max * dh, 0, status, st));
 }
 
 dv_status dv_sparse_mlp_q8(const float* y, int B, int d, int N, const int8_t* W1q, const float* W1s, const float* b1,

@@ -1,0 +1,218 @@
+// Paged key-value cache: argument checks, launches and C entry points.
+// Declarations and argument contracts: include/dejavu.h.
+#include "dv_paged.cuh"
+#include "dv_launch.cuh"
+
+namespace dv {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int CTAS_PER_SM = 2;  // of the attention kernel, at most
+
+bool dtype_ok(int t) { return t == DV_F32 || t == DV_BF16; }
+int blocks64(int dh) { return dh <= 64 ? 1 : dh <= 128 ? 2 : 4; }
+
+template <typename KT, int NB, int NT>
+cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
+  constexpr int PARTF = NT * (NB * 4 + 1) * 128;
+  constexpr int per_sm = sizeof(KT) == 2 && NB <= 2 && NT == 1 ? CTAS_PER_SM : 1;
+  a.NQ = (a.G + 8 * NT - 1) / (8 * NT);
+  const size_t smem = PGA_WARPS * (PARTF * 4ull + NT * NB * 4 * 3 * 32 * 8ull) + 4ull * (2 * a.B + 1);
+  cudaError_t e = allow_smem(paged_attn_kernel<KT, NB, NT>, smem);
+  if (e != cudaSuccess) return e;
+  const long long cap = (long long)a.W * a.page;
+  const long long most = a.B * ((cap + PGA_UNIT - 1) / PGA_UNIT) * (long long)a.rows * a.NQ;  // units, at most
+  const long long want = (most + PGA_WARPS - 1) / PGA_WARPS, have = (long long)sm_count() * per_sm;
+  return launch_main(paged_attn_kernel<KT, NB, NT>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
+                     dim3(PGA_THREADS), smem, st, a);
+}
+
+template <typename KT>
+cudaError_t launch_attn_kt(const PagedAttnArgs& a, cudaStream_t st) {
+  switch (blocks64(a.dh)) {
+    case 1: return a.G > 8 ? launch_attn<KT, 1, 2>(a, st) : launch_attn<KT, 1, 1>(a, st);
+    case 2: return a.G > 8 ? launch_attn<KT, 2, 2>(a, st) : launch_attn<KT, 2, 1>(a, st);
+    default: return launch_attn<KT, 4, 1>(a, st);
+  }
+}
+
+long long stride_rows(const dv_paged_kv* kv) {
+  return kv->page_stride ? kv->page_stride / kv->dh : (long long)kv->h_kv * kv->page;
+}
+
+}  // namespace
+
+size_t paged_attn_part_floats(int dh) {
+  const int nb = blocks64(dh);
+  return (size_t)CTAS_PER_SM * sm_count() * 2 * (nb == 4 ? 1 : 2) * (nb * 4 + 1) * 128;
+}
+
+dv_status paged_kv_check(const dv_paged_kv* kv) {
+  if (!kv || !kv->K || !kv->V || !dtype_ok(kv->kvdtype)) return DV_ERR_ARG;
+  if (!aligned16(kv->K) || !aligned16(kv->V)) return DV_ERR_ALIGN;
+  if (kv->n_pages < 1 || kv->page < 1 || kv->h_kv < 1 || kv->dh < 8 || kv->dh % 8 != 0 || kv->page_stride < 0)
+    return DV_ERR_ARG;
+  const long long need = (long long)kv->h_kv * kv->page * kv->dh;
+  if (kv->page_stride && (kv->page_stride < need || kv->page_stride % kv->dh != 0)) return DV_ERR_ARG;
+  // rows of dh elements and token slots are numbered with 32 bits
+  if (kv->dh > PAGED_MAX_DH || stride_rows(kv) > INT32_MAX / kv->n_pages || kv->page > INT32_MAX / kv->n_pages)
+    return DV_ERR_UNSUPPORTED;
+  return DV_OK;
+}
+
+cudaError_t run_paged_attn(const dv_paged_kv* kv, const float* q, int B, int rows, int G, const int32_t* table, int W,
+                           const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
+                           float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st) {
+  PagedAttnArgs a = {};
+  a.q = q;
+  a.K = kv->K;
+  a.V = kv->V;
+  a.table = table;
+  a.lens = lens;
+  a.head_idx = head_idx;
+  a.head_count = head_count;
+  a.out = out;
+  a.lse = lse;
+  a.part = part;
+  a.tick = tick;
+  a.status = status;
+  a.B = B;
+  a.W = W;
+  a.rows = rows;
+  a.G = G;
+  a.h_kv = kv->h_kv;
+  a.dh = kv->dh;
+  a.page = kv->page;
+  a.page_shift = (kv->page & (kv->page - 1)) == 0 ? __builtin_ctz((unsigned)kv->page) : -1;
+  a.n_pages = kv->n_pages;
+  a.stride_rows = (int)stride_rows(kv);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return kv->kvdtype == DV_BF16 ? launch_attn_kt<bf16>(a, st) : launch_attn_kt<float>(a, st);
+}
+
+cudaError_t run_paged_token(const dv_paged_kv* kv, const void* ks, const void* vs, const int32_t* slots, int B,
+                            const int32_t* head_idx, const int32_t* head_count, int kh_max, int all, float* out, int d,
+                            int* status, cudaStream_t st) {
+  PagedTokenArgs a = {};
+  a.ks = ks;
+  a.vs = vs;
+  a.slots = slots;
+  a.head_idx = head_idx;
+  a.head_count = head_count;
+  a.K = kv->K;
+  a.V = kv->V;
+  a.out = out;
+  a.status = status;
+  a.h = kv->h_kv;
+  a.dh8 = kv->dh / 8;
+  a.page = kv->page;
+  a.stride_rows = (int)stride_rows(kv);
+  a.n_slots = kv->n_pages * kv->page;
+  a.kh_max = kh_max;
+  a.all = all;
+  a.d = d;
+  const int vecs = a.h * a.dh8 * (kv->kvdtype == DV_BF16 ? 1 : 2);
+  const dim3 grid((unsigned)((vecs + PA_THREADS - 1) / PA_THREADS), (unsigned)B);
+  return kv->kvdtype == DV_BF16 ? launch(paged_token_kernel<bf16>, grid, dim3(PA_THREADS), 0, st, a)
+                                : launch(paged_token_kernel<float>, grid, dim3(PA_THREADS), 0, st, a);
+}
+
+}  // namespace dv
+
+using namespace dv;
+
+namespace {
+
+dv_status ws_check(void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return DV_ERR_ARG;
+  if (!aligned16(ws)) return DV_ERR_ALIGN;
+  return ws_bytes < need ? DV_ERR_WORKSPACE : DV_OK;
+}
+
+dv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DV_OK : DV_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+dv_status dv_page_tables(const int32_t* want, int R, int page, int n_pages, int W, const int32_t* lens,
+                         int32_t* lens_out, int32_t* table, int32_t* free_list, const int32_t* free_count,
+                         int32_t* free_count_out, int max_tokens, int32_t* slots, int32_t* offsets, int32_t* granted,
+                         void* ws, size_t ws_bytes, dv_stream_t stream) {
+  if (!want || !lens || !lens_out || !table || !free_list || !free_count || !free_count_out || !offsets || !granted)
+    return DV_ERR_ARG;
+  if (R < 1 || page < 1 || n_pages < 1 || W < 1 || max_tokens < 0 || (max_tokens > 0 && !slots)) return DV_ERR_ARG;
+  for (const void* p : {(const void*)want, (const void*)lens, (const void*)lens_out, (const void*)table,
+                        (const void*)free_list, (const void*)free_count, (const void*)free_count_out,
+                        (const void*)slots, (const void*)offsets, (const void*)granted})
+    if (!ok_opt(p)) return DV_ERR_ALIGN;
+  // tokens, slots and pages of all requests are counted with 31 bits
+  if (R > PAGED_MAX_ROWS || page > INT32_MAX / n_pages || page > INT32_MAX / R / W || max_tokens > INT32_MAX - 4)
+    return DV_ERR_UNSUPPORTED;
+  const dv_status s = ws_check(ws, ws_bytes, WS_HEADER);
+  if (s != DV_OK) return s;
+  PageTablesArgs a = {want, lens, lens_out, table, free_list, free_count, free_count_out, slots, offsets, granted,
+                      static_cast<int*>(ws), R, W, page, n_pages, max_tokens};
+  const size_t smem = 16ull * (R + 1);
+  cudaError_t e = allow_smem(page_tables_kernel, smem);
+  if (e != cudaSuccess) return DV_ERR_CUDA;
+  const int cs = R > 1024 || max_tokens > 4096 ? 8 : 1;
+  return cuda_status(launch_cluster(page_tables_kernel, dim3(cs), dim3(PT_THREADS), smem,
+                                    reinterpret_cast<cudaStream_t>(stream), cs, a));
+}
+
+dv_status dv_paged_append(const dv_paged_kv* kv, const float* k, const float* v, int T, const int32_t* slots, void* ws,
+                          size_t ws_bytes, dv_stream_t stream) {
+  dv_status s = paged_kv_check(kv);
+  if (s != DV_OK) return s;
+  if (T < 0 || !k || !v || !slots) return DV_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return DV_ERR_ALIGN;
+  s = ws_check(ws, ws_bytes, WS_HEADER);
+  if (s != DV_OK) return s;
+  if (T == 0) return DV_OK;
+  PagedAppendArgs a = {};
+  a.k = k;
+  a.v = v;
+  a.slots = slots;
+  a.K = kv->K;
+  a.V = kv->V;
+  a.status = static_cast<int*>(ws);
+  a.h = kv->h_kv;
+  a.dh8 = kv->dh / 8;
+  a.chunks = (long long)T * a.h * a.dh8;
+  a.page = kv->page;
+  a.stride_rows = (int)stride_rows(kv);
+  a.n_slots = kv->n_pages * kv->page;
+  const long long grid = (a.chunks + PA_THREADS - 1) / PA_THREADS;
+  if (grid > INT32_MAX) return DV_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(kv->kvdtype == DV_BF16
+                         ? launch(paged_append_kernel<bf16>, dim3((unsigned)grid), dim3(PA_THREADS), 0, st, a)
+                         : launch(paged_append_kernel<float>, dim3((unsigned)grid), dim3(PA_THREADS), 0, st, a));
+}
+
+dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, const int32_t* table, int W,
+                        const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
+                        int kh_max, float* out, float* lse, void* ws, size_t ws_bytes, dv_stream_t stream) {
+  dv_status s = paged_kv_check(kv);
+  if (s != DV_OK) return s;
+  if (!q || !table || !lens || !out || B < 1 || W < 1 || h_q < 1 || h_q % kv->h_kv != 0) return DV_ERR_ARG;
+  if ((head_idx != nullptr) != (head_count != nullptr)) return DV_ERR_ARG;
+  if (head_idx && (kh_max < 0 || kh_max > kv->h_kv)) return DV_ERR_ARG;
+  for (const void* p : {(const void*)q, (const void*)table, (const void*)lens, (const void*)head_idx,
+                        (const void*)head_count, (const void*)out, (const void*)lse})
+    if (!ok_opt(p)) return DV_ERR_ALIGN;
+  if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - PGA_UNIT) / W) return DV_ERR_UNSUPPORTED;
+  if (((long long)W * kv->page + PGA_UNIT) / PGA_UNIT * B > INT32_MAX) return DV_ERR_UNSUPPORTED;
+  s = ws_check(ws, ws_bytes, WS_HEADER + 4 * paged_attn_part_floats(kv->dh));
+  if (s != DV_OK) return s;
+  if (head_idx && kh_max == 0) return DV_OK;
+  char* w = static_cast<char*>(ws);
+  return cuda_status(run_paged_attn(kv, q, B, head_idx ? kh_max : kv->h_kv, h_q / kv->h_kv, table, W, lens, scale,
+                                    head_idx, head_count, out, lse, reinterpret_cast<float*>(w + WS_HEADER),
+                                    reinterpret_cast<unsigned*>(w + WS_TICKETS), reinterpret_cast<int*>(w),
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -82,8 +82,9 @@ enum {
   DV_DEV_COUNT_CLAMPED = 1, /* a device count exceeded its bound */
   DV_DEV_INDEX_RANGE = 2,   /* a selected index was outside [0, n); skipped */
   DV_DEV_BAD_PARTIAL = 4,   /* attention combine found no partial for a head */
-  DV_DEV_TIMEOUT = 8        /* a bounded wait inside a kernel ran out (about 2 s); the kernel
+  DV_DEV_TIMEOUT = 8,       /* a bounded wait inside a kernel ran out (about 2 s); the kernel
                                stopped early and its outputs are incomplete */
+  DV_DEV_REFUSED = 16       /* dv_page_tables refused a request's growth (see `granted`) */
 };
 
 /* Opaque stream handle; pass a cudaStream_t. */
@@ -109,11 +110,18 @@ typedef enum {
   DV_OP_TOPK = 2,
   DV_OP_SPARSE_MLP = 3,
   DV_OP_SPARSE_MHA = 4,
-  DV_OP_DECODE_LAYER = 5
+  DV_OP_DECODE_LAYER = 5,
+  DV_OP_PAGE_TABLES = 6,
+  DV_OP_PAGED_APPEND = 7,
+  DV_OP_PAGED_ATTN = 8,
+  DV_OP_SPARSE_MHA_PAGED = 9
 } dv_op;
 
 /* Bytes of workspace an operation needs for the given sizes (0 if the sizes
- * are invalid). For DV_OP_TOPK, dims->N is the score row length. */
+ * are invalid). For DV_OP_TOPK, dims->N is the score row length. For
+ * DV_OP_PAGED_ATTN only dims->dh counts; DV_OP_PAGE_TABLES and
+ * DV_OP_PAGED_APPEND need the same whatever the sizes; DV_OP_SPARSE_MHA_PAGED
+ * takes B, d, h, dh and kh_max. */
 DV_API size_t dv_workspace_size(int op, const dv_dims* dims);
 
 /* Text of a status code (static storage). */
@@ -411,6 +419,111 @@ DV_API dv_status dv_prefetch_layer(const dv_layer_weights* w, const dv_dims* dim
 #define DV_TOPK_STATIC_SCRATCH_BYTES (256 + 4 * DV_TOPK_STATIC_MAX_ROWS * (DV_TOPK_STATIC_MAX_N / 32))
 DV_API dv_status dv_topk_static(const float* scores, int B, int n, int k, float tau, int mode, int32_t* idx,
                                 int32_t* count, dv_stream_t stream);
+
+/* -------------------------------------------------------------------------
+ * Paged key-value cache: requests of different lengths share pools of pages
+ * of `page` tokens. Row r of a block table lists request r's pages in order,
+ * so its token s lies in page table[r][s / page] at place s % page; a token's
+ * slot is page index * page + place. (The calls above keep one contiguous
+ * cache per batch row and one position for all rows; the pages cite no such
+ * cache, this is the layout that serves several requests at once.)
+ *
+ * A decode loop calls, once per step, dv_page_tables with the requests' new
+ * lengths, and then per layer dv_sparse_mha_paged, or its own projections
+ * with dv_paged_append and dv_paged_attn. Block tables, lengths and slots are
+ * int32 in device memory; nothing is read back to the host, and all of these
+ * calls can be captured into a CUDA graph (the sizes given are bounds).
+ * ------------------------------------------------------------------------- */
+
+/* The pools. Head i, token s, channel c of page p is element
+ * p * page_stride + (i * page + s) * dh + c of K and of V: one head's rows of
+ * a page are contiguous. page_stride = 0 stands for h_kv * page * dh; a larger
+ * one (a multiple of dh) lets several layers, or K and V, share one pool.
+ * dh is a multiple of 8 up to 256; n_pages * page and n_pages * page_stride /
+ * dh must be below 2^31 (DV_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  dv_dtype kvdtype;
+  void* K;
+  void* V;
+  long long page_stride; /* elements from a page to the next, or 0 */
+  int n_pages;
+  int page; /* tokens per page, any size >= 1 */
+  int h_kv; /* key-value heads */
+  int dh;
+} dv_paged_kv;
+
+/* Block tables and slot maps from request lengths. For each request r < R
+ * (R <= 4096): lens[r] tokens are in its pages; want[r] is the length it should have,
+ * negative: leave it as it is. With pages(n) = ceil(n / page):
+ *  - a request that shrinks (want < lens; 0 releases it) gives back its pages
+ *    from pages(want) on; they are pushed on the free stack free_list
+ *    [n_pages] (its first *free_count entries are free) in request order, each
+ *    request's pages in order;
+ *  - a request that grows takes pages(want) - pages(lens) pages from the top
+ *    of that stack, in request order, each page from the next entry down.
+ *    Pages given back in the same call can be taken. It is granted if it
+ *    needs no page or the pages needed by the requests up to and including it
+ *    are available, and the tokens added by them fit max_tokens; else it keeps
+ *    its length and pages (granted[r] = 0, DV_DEV_REFUSED is set). A want
+ *    above W * page is refused too and counts nothing for the requests after it.
+ * Out: lens_out [R] the new lengths; granted [R] 1 or 0; table [R][W] gets the
+ * pages taken (other entries, those given back too, stay as they were);
+ * offsets [R + 1] the running sum of tokens added; slots [max_tokens] the slot
+ * of every token added, request after request, -1 after the last;
+ * free_list; *free_count_out the free pages left. lens_out may be lens and
+ * free_count_out may be free_count (other arrays must not overlap); kept
+ * apart, a repeated call gives the same result again.
+ * A length outside [0, W * page] is kept, refused and flagged (DV_DEV_INDEX_RANGE);
+ * a free count outside [0, n_pages] is clamped and flagged. */
+DV_API dv_status dv_page_tables(const int32_t* want, int R, int page, int n_pages, int W, const int32_t* lens,
+                                int32_t* lens_out, int32_t* table, int32_t* free_list, const int32_t* free_count,
+                                int32_t* free_count_out, int max_tokens, int32_t* slots, int32_t* offsets,
+                                int32_t* granted, void* ws, size_t ws_bytes, dv_stream_t stream);
+
+/* Stores the keys and values of T tokens: k, v [T][h_kv][dh] fp32, rounded to
+ * the pools' dtype, into slots[t] (device int32). A negative slot is passed
+ * over (padding); one outside the pools is passed over and flagged
+ * (DV_DEV_INDEX_RANGE). Two tokens must not have the same slot (which of them
+ * is kept is not defined). */
+DV_API dv_status dv_paged_append(const dv_paged_kv* kv, const float* k, const float* v, int T, const int32_t* slots,
+                                 void* ws, size_t ws_bytes, dv_stream_t stream);
+
+/* Attention of one new token per request over its pages (eq. (2)'s H_i without
+ * the projections; B <= 4096):
+ *   out[b][i] = softmax(scale q[b][i] K_b^T) V_b over the request's first
+ *   lens[b] tokens, those of the new token included (append it first).
+ * q, out [B][h_q][dh] fp32; h_q is a multiple of h_kv, and query head i reads
+ * key-value head i / (h_q / h_kv). table [B][W]. A length of 0 or below gives
+ * zeros; one above W * page is clamped and flagged (DV_DEV_COUNT_CLAMPED).
+ * lse: NULL, or [B][h_q] fp32: log of the sum of exp(scale q . K), minus
+ * infinity where there is none, to join with attention over other keys.
+ * head_idx / head_count: NULL, or a set of key-value heads (device, bounded by
+ * kh_max): only those are read, and q, out are [B][kh_max][h_q / h_kv][dh] (lse
+ * without dh), entry j belonging to head head_idx[j]; entries from the count
+ * on are left as they were. Slots past a request's length are never used,
+ * whatever they hold. A page or head index out of range leaves its keys
+ * out and is flagged (DV_DEV_INDEX_RANGE). Finite q, K and V are assumed
+ * where they are used; results do not depend on the order in which CTAs end. */
+DV_API dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, const int32_t* table, int W,
+                               const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
+                               int kh_max, float* out, float* lse, void* ws, size_t ws_bytes, dv_stream_t stream);
+
+/* dv_sparse_mha over a paged cache, every batch row with its own length: for
+ * the heads in head_idx, q, k, v of the new token are computed, k and v are
+ * stored in slots[b] (from dv_page_tables; negative: not stored), the
+ * attention runs over lens[b] tokens (the new one included), and
+ *   out[b] (+)= sum_{i in S_A} H_i WOt[i] (+ bO).
+ * y, Wqkv, bqkv, WOt, bO, head_idx, head_count, kh_max, out, accumulate as
+ * for dv_sparse_mha (h = kv->h_kv heads, dh 64 or 128, kv->kvdtype = wdtype,
+ * h <= 1024). exact_kv nonzero: k and v of the unselected heads are computed
+ * and stored too; 0: their place in slots[b] is set to zero, since a recycled page
+ * holds another request's keys and values. A row of length 0 gets bO alone. */
+DV_API dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, const float* bqkv,
+                                     const void* WOt, const float* bO, dv_dtype wdtype, const dv_paged_kv* kv,
+                                     const int32_t* table, int W, const int32_t* lens, const int32_t* slots,
+                                     float scale, const int32_t* head_idx, const int32_t* head_count, int kh_max,
+                                     float* out, int accumulate, int exact_kv, void* ws, size_t ws_bytes,
+                                     dv_stream_t stream);
 
 /* Number of kernels this library has launched in this process (host-side
  * counter, for reporting). */
