@@ -16,13 +16,14 @@ int blocks64(int dh) { return dh <= 64 ? 1 : dh <= 128 ? 2 : 4; }
 template <typename KT, int NB, int NT>
 cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
   constexpr int PARTF = NT * (NB * 4 + 1) * 128;
-  constexpr int per_sm = sizeof(KT) == 2 && NB <= 2 && NT == 1 ? CTAS_PER_SM : 1;
+  constexpr int per_sm = PagedShape<KT, NB, NT>::CTAS, UNIT = PagedShape<KT, NB, NT>::UNIT;
+  static_assert(per_sm <= CTAS_PER_SM, "partial slots");
   a.NQ = (a.G + 8 * NT - 1) / (8 * NT);
   const size_t smem = PGA_WARPS * (PARTF * 4ull + NT * NB * 4 * 3 * 32 * 8ull) + 4ull * (2 * a.B + 1);
   cudaError_t e = allow_smem(paged_attn_kernel<KT, NB, NT>, smem);
   if (e != cudaSuccess) return e;
   const long long cap = (long long)a.W * a.page;
-  const long long most = a.B * ((cap + PGA_UNIT - 1) / PGA_UNIT) * (long long)a.rows * a.NQ;  // units, at most
+  const long long most = a.B * ((cap + UNIT - 1) / UNIT) * (long long)a.rows * a.NQ;  // units, at most
   const long long want = (most + PGA_WARPS - 1) / PGA_WARPS, have = (long long)sm_count() * per_sm;
   return launch_main(paged_attn_kernel<KT, NB, NT>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
                      dim3(PGA_THREADS), smem, st, a);
@@ -203,8 +204,8 @@ dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, c
   for (const void* p : {(const void*)q, (const void*)table, (const void*)lens, (const void*)head_idx,
                         (const void*)head_count, (const void*)out, (const void*)lse})
     if (!ok_opt(p)) return DV_ERR_ALIGN;
-  if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - PGA_UNIT) / W) return DV_ERR_UNSUPPORTED;
-  if (((long long)W * kv->page + PGA_UNIT) / PGA_UNIT * B > INT32_MAX) return DV_ERR_UNSUPPORTED;
+  if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - 32) / W) return DV_ERR_UNSUPPORTED;
+  if (((long long)W * kv->page + 16) / 16 * B > INT32_MAX) return DV_ERR_UNSUPPORTED;  // units of all rows
   s = ws_check(ws, ws_bytes, WS_HEADER + 4 * paged_attn_part_floats(kv->dh));
   if (s != DV_OK) return s;
   if (head_idx && kh_max == 0) return DV_OK;

@@ -336,7 +336,6 @@ __global__ void __launch_bounds__(PA_THREADS) paged_token_kernel(PagedTokenArgs 
 // ----------------------------------------------------------------------------
 constexpr int PGA_WARPS = 8;
 constexpr int PGA_THREADS = PGA_WARPS * 32;
-constexpr int PGA_UNIT = 16;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -364,11 +363,16 @@ struct PagedAt {
   int b, it, t, nt;
 };
 
-// Eight channels of a cache row in registers (zeros where the row is masked).
+// Eight channels of a cache row in registers.
 template <typename KT>
 struct Chunk {
   static constexpr int N = sizeof(KT) / 2;
   uint4 v[N];
+  __device__ __forceinline__ void load(const KT* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
+  }
+  // zeros where the row is masked or the channels lie past dh
   __device__ __forceinline__ void load(const KT* pool, int row, int dh8, int c) {
     const uint4* p = reinterpret_cast<const uint4*>(pool) + ((long long)row * dh8 + c) * N;
 #pragma unroll
@@ -380,10 +384,22 @@ struct Chunk {
   }
 };
 
+// Shape of a kernel for NB blocks of 64 channels and NT tiles of 8 query heads:
+// 16-key tiles in a unit, CTAs per SM.
 template <typename KT, int NB, int NT>
-__global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT == 1) ? 2 : 1)
+struct PagedShape {
+  static constexpr int BYTES = sizeof(KT) * NB;  // a tile's K row bytes / 64
+  static constexpr int MT = BYTES <= 4 && NT == 1 ? 2 : 1;
+  static constexpr int CTAS = BYTES == 2 && NT == 1 ? 2 : 1;
+  static constexpr int UNIT = 16 * MT;
+};
+
+template <typename KT, int NB, int NT>
+__global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr bool F32 = sizeof(KT) == 4;
+  constexpr int MT = PagedShape<KT, NB, NT>::MT, UNIT = 16 * MT;
+  constexpr int DH = 64 * NB;                // channels, padded
   constexpr int SPL = F32 ? 3 : 1;           // bf16 terms of a cache element
   constexpr int NC = 2 * NB;                 // K chunks a lane holds per row
   constexpr int NK = 4 * NB;                 // MMA steps over the channels
@@ -419,7 +435,7 @@ __global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT
       if (blockIdx.x == 0) raise_status(a.status, ST_CLAMPED);
     }
     unsigned tot;
-    const unsigned ex = block_exclusive_scan<PGA_THREADS>(len > 0 ? (unsigned)((len + PGA_UNIT - 1) / PGA_UNIT) : 0u, sc, &tot);
+    const unsigned ex = block_exclusive_scan<PGA_THREADS>(len > 0 ? (unsigned)((len + UNIT - 1) / UNIT) : 0u, sc, &tot);
     if (r < a.B) {
       s_pre[r] = base + ex;
       s_len[r] = len;
@@ -464,9 +480,9 @@ __global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT
     p.it = 0;
     do { ++p.b; } while ((p.nt = s_pre[p.b + 1] - s_pre[p.b]) == 0);
   };
-  // The pool row of key (lane & 15) of a unit, -1 where masked
+  // The pool row of key `lane` of a unit (of 16: both halves of the warp alike), -1 where masked
   auto pool_row = [&](const PagedAt& p) {
-    const int key = p.t * PGA_UNIT + (lane & 15);
+    const int key = p.t * UNIT + (lane & (UNIT - 1));
     if (key >= s_len[p.b]) return -1;
     const int j = p.it / a.NQ;
     const int head = a.head_idx ? a.head_idx[j] : j;
@@ -480,27 +496,53 @@ __global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT
   };
 
   float o[NT][NB][4][4], m[NT][2], l[NT][2];
-  Chunk<KT> kc[2][NC], vc[NB][4];
-  bool ok0 = false, ok1 = false;  // keys g and g + 8 of the unit in kc are not masked
-  int vrow[4];
+  Chunk<KT> kc[2 * MT][NC], vc[NB][4 * MT];
+  unsigned ok = 0;  // keys g + 8 i of the unit in kc that are not masked
+  // Whole pages of 16-key tiles and channels without padding: a tile's rows are
+  // consecutive, so a lane's loads are one pointer and constant offsets.
+  const bool tiled = a.dh == DH && (a.page & 15) == 0;
 
   auto load_k = [&](int row) {
-    const int r0 = __shfl_sync(0xffffffffu, row, g), r1 = __shfl_sync(0xffffffffu, row, g + 8);
-    ok0 = r0 >= 0;
-    ok1 = r1 >= 0;
+    if (tiled && __all_sync(0xffffffffu, row >= 0)) {
+      ok = ~0u;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      kc[0][i].load(Kp, r0, dh8, t4 + 4 * i);
-      kc[1][i].load(Kp, r1, dh8, t4 + 4 * i);
+      for (int mt = 0; mt < MT; ++mt) {
+        const KT* p = Kp + (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + g) * DH + 8 * t4;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          kc[2 * mt][i].load(p + 32 * i);
+          kc[2 * mt + 1][i].load(p + 8 * DH + 32 * i);
+        }
+      }
+    } else {
+      ok = 0;
+#pragma unroll
+      for (int j = 0; j < 2 * MT; ++j) {
+        const int r = __shfl_sync(0xffffffffu, row, g + 8 * j);
+        ok |= r >= 0 ? 1u << j : 0u;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) kc[j][i].load(Kp, r, dh8, t4 + 4 * i);
+      }
     }
   };
-  auto rows_v = [&](int row) {
+  auto load_v = [&](int row, int nb0, int nb1) {
+    if (tiled && __all_sync(0xffffffffu, row >= 0)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) vrow[i] = __shfl_sync(0xffffffffu, row, 2 * t4 + (i & 1) + (i >> 1) * 8);
-  };
-  auto load_v = [&](int nb) {
+      for (int mt = 0; mt < MT; ++mt) {
+        const KT* p = Vp + (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + 2 * t4) * DH + 8 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) vc[nb][i].load(Vp, vrow[i], dh8, g + 8 * nb);
+        for (int nb = nb0; nb < nb1; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vc[nb][4 * mt + i].load(p + ((i & 1) + (i >> 1) * 8) * DH + 64 * nb);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4 * MT; ++j) {
+        const int r = __shfl_sync(0xffffffffu, row, 2 * t4 + (j & 1) + (j >> 1) * 8);
+#pragma unroll
+        for (int nb = nb0; nb < nb1; ++nb) vc[nb][j].load(Vp, r, dh8, g + 8 * nb);
+      }
+    }
   };
   uint2* q_mine = s_q + warp * NT * NK * 3 * 32 + lane;
 
@@ -610,128 +652,143 @@ __global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT
   if (wlo < whi) {
     cur = locate(wlo);
     PagedAt nxt = cur;
+    const int count = (int)(whi - wlo);
     int row = pool_row(cur);
     if (PRE) {
       load_k(row);
-      rows_v(row);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) load_v(nb);
+      load_v(row, 0, NB);
     }
-    if (wlo + 1 < whi) {
+    if (count > 1) {
       advance(nxt);
       if (PRE) row = pool_row(nxt);
     }
     started = cur.t == 0;
     begin_item(cur);
-    for (long long u = wlo; u < whi; ++u) {
-      const bool more = u + 1 < whi;
-      if (!PRE) {
-        load_k(row);
-        rows_v(row);
-      }
-      // scores of 16 keys by 8 NT queries
-      float s[NT][4];
+#pragma unroll 1
+    for (int n = 0; n < count; ++n) {
+      const bool more = n + 1 < count;
+      if (!PRE) load_k(row);
+      // scores of UNIT keys by 8 NT queries
+      float s[NT][MT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float hi[2][4] = {}, lo[4] = {};
+        float hi[MT][2][4] = {}, lo[MT][4] = {};
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-          const Chunk<KT>&x = kc[0][k >> 1], &y = kc[1][k >> 1];
-          uint32_t f[SPL][4];
-          const int w = (k & 1) * 2 * SPL / (F32 ? 3 : 1);  // first word: 2 per half (bf16)
-          if constexpr (!F32) {
-            f[0][0] = x.word(w);
-            f[0][1] = y.word(w);
-            f[0][2] = x.word(w + 1);
-            f[0][3] = y.word(w + 1);
-          } else {
-            const int e = (k & 1) * 4;
-            split3(__uint_as_float(x.word(e)), __uint_as_float(x.word(e + 1)), f[0][0], f[1][0], f[2][0]);
-            split3(__uint_as_float(y.word(e)), __uint_as_float(y.word(e + 1)), f[0][1], f[1][1], f[2][1]);
-            split3(__uint_as_float(x.word(e + 2)), __uint_as_float(x.word(e + 3)), f[0][2], f[1][2], f[2][2]);
-            split3(__uint_as_float(y.word(e + 2)), __uint_as_float(y.word(e + 3)), f[0][3], f[1][3], f[2][3]);
-          }
           const uint2* qd = q_mine + (nt * NK + k) * 3 * 32;
           const uint2 q0 = qd[0], q1 = qd[32], q2 = qd[64];
-          mma_bf16(lo, f[0], q2.x, q2.y);
-          if constexpr (F32) {
-            mma_bf16(lo, f[2], q0.x, q0.y);
-            mma_bf16(lo, f[1], q1.x, q1.y);
-            mma_bf16(lo, f[1], q0.x, q0.y);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const Chunk<KT>&x = kc[2 * mt][k >> 1], &y = kc[2 * mt + 1][k >> 1];
+            uint32_t f[SPL][4];
+            if constexpr (!F32) {
+              const int w = (k & 1) * 2;
+              f[0][0] = x.word(w);
+              f[0][1] = y.word(w);
+              f[0][2] = x.word(w + 1);
+              f[0][3] = y.word(w + 1);
+            } else {
+              const int e = (k & 1) * 4;
+              split3(__uint_as_float(x.word(e)), __uint_as_float(x.word(e + 1)), f[0][0], f[1][0], f[2][0]);
+              split3(__uint_as_float(y.word(e)), __uint_as_float(y.word(e + 1)), f[0][1], f[1][1], f[2][1]);
+              split3(__uint_as_float(x.word(e + 2)), __uint_as_float(x.word(e + 3)), f[0][2], f[1][2], f[2][2]);
+              split3(__uint_as_float(y.word(e + 2)), __uint_as_float(y.word(e + 3)), f[0][3], f[1][3], f[2][3]);
+            }
+            mma_bf16(lo[mt], f[0], q2.x, q2.y);
+            if constexpr (F32) {
+              mma_bf16(lo[mt], f[2], q0.x, q0.y);
+              mma_bf16(lo[mt], f[1], q1.x, q1.y);
+              mma_bf16(lo[mt], f[1], q0.x, q0.y);
+            }
+            mma_bf16(lo[mt], f[0], q1.x, q1.y);
+            mma_bf16(hi[mt][k & 1], f[0], q0.x, q0.y);
           }
-          mma_bf16(lo, f[0], q1.x, q1.y);
-          mma_bf16(hi[k & 1], f[0], q0.x, q0.y);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = ((i < 2 ? ok0 : ok1)) ? (hi[0][i] + hi[1][i] + lo[i]) * a.scale_log2 : -INFINITY;
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[nt][mt][i] = (ok >> (2 * mt + (i >> 1))) & 1 ? (hi[mt][0][i] + hi[mt][1][i] + lo[mt][i]) * a.scale_log2 : -INFINITY;
       }
       if (PRE && more) load_k(row);
       // running maximum and sum; p in bf16 terms, transposed into B fragments
-      uint32_t pf[NT][3][2];
+      uint32_t pf[NT][MT][3][2];
       float corr[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = fmaxf(s[nt][i], s[nt][2 + i]);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[nt][mt][i], s[nt][mt][2 + i]));
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
           const float mn = fmaxf(m[nt][i], mx), mu = mn == -INFINITY ? 0.f : mn;
           corr[nt][i] = exp2f(m[nt][i] - mu);
           m[nt][i] = mn;
-          s[nt][i] = exp2f(s[nt][i] - mu);
-          s[nt][2 + i] = exp2f(s[nt][2 + i] - mu);
-          l[nt][i] = l[nt][i] * corr[nt][i] + (s[nt][i] + s[nt][2 + i]);
+          float sum = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            s[nt][mt][i] = exp2f(s[nt][mt][i] - mu);
+            s[nt][mt][2 + i] = exp2f(s[nt][mt][2 + i] - mu);
+            sum += s[nt][mt][i] + s[nt][mt][2 + i];
+          }
+          l[nt][i] = l[nt][i] * corr[nt][i] + sum;
         }
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t h, mm, ll;
-          split3(s[nt][2 * hf], s[nt][2 * hf + 1], h, mm, ll);
-          pf[nt][0][hf] = transpose8x8(h);
-          pf[nt][1][hf] = transpose8x8(mm);
-          pf[nt][2][hf] = transpose8x8(ll);
-        }
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t h, mm, ll;
+            split3(s[nt][mt][2 * hf], s[nt][mt][2 * hf + 1], h, mm, ll);
+            pf[nt][mt][0][hf] = transpose8x8(h);
+            pf[nt][mt][1][hf] = transpose8x8(mm);
+            pf[nt][mt][2][hf] = transpose8x8(ll);
+          }
       }
       // o = o corr + V^T p
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        if (!PRE) load_v(nb);
+        if (!PRE) load_v(row, nb, nb + 1);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t f[SPL][4];
-          if constexpr (!F32) {
-            const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-            f[0][0] = __byte_perm(vc[nb][0].word(e >> 1), vc[nb][1].word(e >> 1), sel);
-            f[0][1] = __byte_perm(vc[nb][0].word(2 + (e >> 1)), vc[nb][1].word(2 + (e >> 1)), sel);
-            f[0][2] = __byte_perm(vc[nb][2].word(e >> 1), vc[nb][3].word(e >> 1), sel);
-            f[0][3] = __byte_perm(vc[nb][2].word(2 + (e >> 1)), vc[nb][3].word(2 + (e >> 1)), sel);
-          } else {
-            split3(__uint_as_float(vc[nb][0].word(e)), __uint_as_float(vc[nb][1].word(e)), f[0][0], f[1][0], f[2][0]);
-            split3(__uint_as_float(vc[nb][0].word(4 + e)), __uint_as_float(vc[nb][1].word(4 + e)), f[0][1], f[1][1], f[2][1]);
-            split3(__uint_as_float(vc[nb][2].word(e)), __uint_as_float(vc[nb][3].word(e)), f[0][2], f[1][2], f[2][2]);
-            split3(__uint_as_float(vc[nb][2].word(4 + e)), __uint_as_float(vc[nb][3].word(4 + e)), f[0][3], f[1][3], f[2][3]);
-          }
+          float c[NT][4] = {};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float c[4] = {};
-            mma_bf16(c, f[0], pf[nt][2][0], pf[nt][2][1]);
-            if constexpr (F32) {
-              mma_bf16(c, f[2], pf[nt][0][0], pf[nt][0][1]);
-              mma_bf16(c, f[1], pf[nt][1][0], pf[nt][1][1]);
-              mma_bf16(c, f[1], pf[nt][0][0], pf[nt][0][1]);
+          for (int mt = 0; mt < MT; ++mt) {
+            const Chunk<KT>* v = vc[nb] + 4 * mt;
+            uint32_t f[SPL][4];
+            if constexpr (!F32) {
+              const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+              f[0][0] = __byte_perm(v[0].word(e >> 1), v[1].word(e >> 1), sel);
+              f[0][1] = __byte_perm(v[0].word(2 + (e >> 1)), v[1].word(2 + (e >> 1)), sel);
+              f[0][2] = __byte_perm(v[2].word(e >> 1), v[3].word(e >> 1), sel);
+              f[0][3] = __byte_perm(v[2].word(2 + (e >> 1)), v[3].word(2 + (e >> 1)), sel);
+            } else {
+              split3(__uint_as_float(v[0].word(e)), __uint_as_float(v[1].word(e)), f[0][0], f[1][0], f[2][0]);
+              split3(__uint_as_float(v[0].word(4 + e)), __uint_as_float(v[1].word(4 + e)), f[0][1], f[1][1], f[2][1]);
+              split3(__uint_as_float(v[2].word(e)), __uint_as_float(v[3].word(e)), f[0][2], f[1][2], f[2][2]);
+              split3(__uint_as_float(v[2].word(4 + e)), __uint_as_float(v[3].word(4 + e)), f[0][3], f[1][3], f[2][3]);
             }
-            mma_bf16(c, f[0], pf[nt][1][0], pf[nt][1][1]);
-            mma_bf16(c, f[0], pf[nt][0][0], pf[nt][0][1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[nt][nb][e][i] = fmaf(o[nt][nb][e][i], corr[nt][i & 1], c[i]);
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t(&pm)[3][2] = pf[nt][mt];
+              mma_bf16(c[nt], f[0], pm[2][0], pm[2][1]);
+              if constexpr (F32) {
+                mma_bf16(c[nt], f[2], pm[0][0], pm[0][1]);
+                mma_bf16(c[nt], f[1], pm[1][0], pm[1][1]);
+                mma_bf16(c[nt], f[1], pm[0][0], pm[0][1]);
+              }
+              mma_bf16(c[nt], f[0], pm[1][0], pm[1][1]);
+              mma_bf16(c[nt], f[0], pm[0][0], pm[0][1]);
+            }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nt][nb][e][i] = fmaf(o[nt][nb][e][i], corr[nt][i & 1], c[nt][i]);
         }
       }
-      if (PRE && more) {
-        rows_v(row);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) load_v(nb);
-      }
+      if (PRE && more) load_v(row, 0, NB);
       const bool ends = cur.t + 1 == cur.nt;
       if (ends || !more) {
         total_l();
@@ -742,8 +799,8 @@ __global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT
         } else if (ends) {  // an item that earlier CTAs began ends in the first warp
           put_part(reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * 2 * PARTF));
           if (lane == 0) {
-            s_join[0][0] = u - cur.t;
-            s_join[0][1] = u;
+            s_join[0][0] = wlo + n - cur.t;
+            s_join[0][1] = wlo + n;
             s_joinat[0][0] = cur.b;
             s_joinat[0][1] = cur.it;
           }
@@ -753,9 +810,9 @@ __global__ void __launch_bounds__(PGA_THREADS, (sizeof(KT) == 2 && NB <= 2 && NT
       }
       if (more) {
         cur = nxt;
-        if (u + 2 < whi) advance(nxt);
+        if (n + 2 < count) advance(nxt);
         if (!PRE) row = pool_row(cur);
-        else if (u + 2 < whi) row = pool_row(nxt);
+        else if (n + 2 < count) row = pool_row(nxt);
         if (ends) {
           started = true;
           begin_item(cur);
