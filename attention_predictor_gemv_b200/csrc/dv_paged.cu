@@ -13,18 +13,44 @@ constexpr int CTAS_PER_SM = 2;  // of the attention kernel, at most
 bool dtype_ok(int t) { return t == DV_F32 || t == DV_BF16; }
 int blocks64(int dh) { return dh <= 64 ? 1 : dh <= 128 ? 2 : 4; }
 
+// Shared memory per SM that the attention asks for: its CTAs' own and no more.
+// Its loads in flight live in the rest, the L1 cache: with the largest shared
+// memory (28 KB of L1) they were bound to 4.8 TB/s.
+template <typename K>
+cudaError_t carve_out(K kern, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int percent = (int)((bytes * 100 + 228 * 1024 - 1) / (228 * 1024));
+  const auto key = std::make_pair(reinterpret_cast<const void*>(kern), dev);
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> set;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = set.find(key);
+  if (it != set.end() && it->second == percent) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, percent > 100 ? 100 : percent);
+  if (e == cudaSuccess) {
+    set[key] = percent;
+    std::lock_guard<std::mutex> lock2(g_carve_mu);
+    g_carve_set[key] = true;  // (launch() leaves it as it is)
+  }
+  return e;
+}
+
 template <typename KT, int NB, int NT>
 cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
-  constexpr int PARTF = NT * (NB * 4 + 1) * 128;
-  constexpr int per_sm = PagedShape<KT, NB, NT>::CTAS, UNIT = PagedShape<KT, NB, NT>::UNIT;
-  static_assert(per_sm <= CTAS_PER_SM, "partial slots");
-  a.NQ = (a.G + 8 * NT - 1) / (8 * NT);
-  const size_t smem = PGA_WARPS * (PARTF * 4ull + NT * NB * 4 * 3 * 32 * 8ull) + 4ull * (2 * a.B + 1);
+  using Shape = PagedShape<KT, NB, NT>;
+  constexpr int per_sm = Shape::CTAS, UNIT = Shape::UNIT;
+  static_assert(per_sm <= CTAS_PER_SM && Shape::PARTF <= 16 * (Shape::DH + 2), "partial slots");
+  a.NQ = (a.G + Shape::QR - 1) / Shape::QR;
+  const size_t smem = PGA_WARPS * (4ull * (Shape::PARTF + Shape::RAWF) + Shape::QBYTES) + 4ull * (2 * a.B + 1);
   cudaError_t e = allow_smem(paged_attn_kernel<KT, NB, NT>, smem);
   if (e != cudaSuccess) return e;
   const long long cap = (long long)a.W * a.page;
   const long long most = a.B * ((cap + UNIT - 1) / UNIT) * (long long)a.rows * a.NQ;  // units, at most
   const long long want = (most + PGA_WARPS - 1) / PGA_WARPS, have = (long long)sm_count() * per_sm;
+  e = carve_out(paged_attn_kernel<KT, NB, NT>, per_sm * (smem + 1024));
+  if (e != cudaSuccess) return e;
   return launch_main(paged_attn_kernel<KT, NB, NT>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
                      dim3(PGA_THREADS), smem, st, a);
 }
@@ -32,9 +58,9 @@ cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
 template <typename KT>
 cudaError_t launch_attn_kt(const PagedAttnArgs& a, cudaStream_t st) {
   switch (blocks64(a.dh)) {
-    case 1: return a.G > 8 ? launch_attn<KT, 1, 2>(a, st) : launch_attn<KT, 1, 1>(a, st);
-    case 2: return a.G > 8 ? launch_attn<KT, 2, 2>(a, st) : launch_attn<KT, 2, 1>(a, st);
-    default: return launch_attn<KT, 4, 1>(a, st);
+    case 1: return a.G == 1 ? launch_attn<KT, 1, 0>(a, st) : a.G > 8 ? launch_attn<KT, 1, 2>(a, st) : launch_attn<KT, 1, 1>(a, st);
+    case 2: return a.G == 1 ? launch_attn<KT, 2, 0>(a, st) : a.G > 8 ? launch_attn<KT, 2, 2>(a, st) : launch_attn<KT, 2, 1>(a, st);
+    default: return a.G == 1 ? launch_attn<KT, 4, 0>(a, st) : launch_attn<KT, 4, 1>(a, st);
   }
 }
 
@@ -45,8 +71,7 @@ long long stride_rows(const dv_paged_kv* kv) {
 }  // namespace
 
 size_t paged_attn_part_floats(int dh) {
-  const int nb = blocks64(dh);
-  return (size_t)CTAS_PER_SM * sm_count() * 2 * (nb == 4 ? 1 : 2) * (nb * 4 + 1) * 128;
+  return (size_t)CTAS_PER_SM * sm_count() * 2 * 16 * (64 * blocks64(dh) + 2);
 }
 
 dv_status paged_kv_check(const dv_paged_kv* kv) {
@@ -205,12 +230,14 @@ dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, c
                         (const void*)head_count, (const void*)out, (const void*)lse})
     if (!ok_opt(p)) return DV_ERR_ALIGN;
   if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - 32) / W) return DV_ERR_UNSUPPORTED;
-  if (((long long)W * kv->page + 16) / 16 * B > INT32_MAX) return DV_ERR_UNSUPPORTED;  // units of all rows
+  const int rows = head_idx ? kh_max : kv->h_kv, G = h_q / kv->h_kv;
+  // the units of all requests and heads are numbered with 31 bits
+  if (((long long)W * kv->page + 16) / 16 * B * ((G + 7) / 8) > INT32_MAX / (rows > 0 ? rows : 1)) return DV_ERR_UNSUPPORTED;
   s = ws_check(ws, ws_bytes, WS_HEADER + 4 * paged_attn_part_floats(kv->dh));
   if (s != DV_OK) return s;
   if (head_idx && kh_max == 0) return DV_OK;
   char* w = static_cast<char*>(ws);
-  return cuda_status(run_paged_attn(kv, q, B, head_idx ? kh_max : kv->h_kv, h_q / kv->h_kv, table, W, lens, scale,
+  return cuda_status(run_paged_attn(kv, q, B, rows, G, table, W, lens, scale,
                                     head_idx, head_count, out, lse, reinterpret_cast<float*>(w + WS_HEADER),
                                     reinterpret_cast<unsigned*>(w + WS_TICKETS), reinterpret_cast<int*>(w),
                                     reinterpret_cast<cudaStream_t>(stream)));

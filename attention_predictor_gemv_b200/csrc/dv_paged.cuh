@@ -338,15 +338,21 @@ constexpr int PGA_WARPS = 8;
 constexpr int PGA_THREADS = PGA_WARPS * 32;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 2^x; what underflows fp32's normal range is 0, nothing next to a weight of 1
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -372,11 +378,9 @@ struct Chunk {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
   }
-  // zeros where the row is masked or the channels lie past dh
-  __device__ __forceinline__ void load(const KT* pool, int row, int dh8, int c) {
-    const uint4* p = reinterpret_cast<const uint4*>(pool) + ((long long)row * dh8 + c) * N;
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = row >= 0 && c < dh8 ? ld_stream(p + i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < N; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ uint32_t word(int i) const {  // i-th 32-bit word
     const uint4& u = v[i >> 2];
@@ -384,38 +388,54 @@ struct Chunk {
   }
 };
 
-// Shape of a kernel for NB blocks of 64 channels and NT tiles of 8 query heads:
-// 16-key tiles in a unit, CTAs per SM.
+// Shape of a kernel for NB blocks of 64 channels and NT groups of 8 query heads
+// (NT = 0: one query head, its bf16 terms in three rows of one group):
+// 16-key tiles in a unit, CTAs per SM, query rows, floats of a partial
+// ([QR][DH] sums, then QR maxima and QR weight sums), bytes of q a warp keeps.
 template <typename KT, int NB, int NT>
 struct PagedShape {
   static constexpr int BYTES = sizeof(KT) * NB;  // a tile's K row bytes / 64
-  static constexpr int MT = BYTES <= 4 && NT == 1 ? 2 : 1;
-  static constexpr int CTAS = BYTES == 2 && NT == 1 ? 2 : 1;
+  static constexpr int MT = BYTES <= 4 && NT <= 1 ? 2 : 1;
+  static constexpr int CTAS = BYTES == 2 && NT <= 1 ? 2 : 1;
   static constexpr int UNIT = 16 * MT;
+  static constexpr int DH = 64 * NB;
+  static constexpr int QR = NT == 0 ? 1 : 8 * NT;
+  static constexpr int PARTF = (QR * (DH + 2) + 3) & ~3;
+  static constexpr int QFRAGS = NT == 0 ? 1 : 2 * NT;
+  static constexpr int QBYTES = QFRAGS * 4 * NB * 32 * 16;
+  static constexpr bool STAGE = NT == 0 || (NT == 1 && NB <= 2);  // the next item's q is copied ahead
+  static constexpr int RAWF = STAGE ? QR * DH : 0;
+  static_assert(QBYTES >= 4 * PARTF, "a warp's last partial takes the place of its q");
 };
 
-template <typename KT, int NB, int NT>
-__global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
+template <typename KT, int NB, int NTQ>
+__global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr bool F32 = sizeof(KT) == 4;
-  constexpr int MT = PagedShape<KT, NB, NT>::MT, UNIT = 16 * MT;
-  constexpr int DH = 64 * NB;                // channels, padded
+  using Shape = PagedShape<KT, NB, NTQ>;
+  constexpr bool F32 = sizeof(KT) == 4, ONE = NTQ == 0;
+  constexpr int NT = ONE ? 1 : NTQ;
+  constexpr int MT = Shape::MT, UNIT = Shape::UNIT, DH = Shape::DH, QR = Shape::QR, PARTF = Shape::PARTF;
   constexpr int SPL = F32 ? 3 : 1;           // bf16 terms of a cache element
+  constexpr int AF = ONE ? 1 : 2;            // A fragments that hold the terms of q, and of p
+  constexpr int EN = F32 || NT > 1 ? 2 : 4;  // channel tiles whose products run side by side
   constexpr int NC = 2 * NB;                 // K chunks a lane holds per row
   constexpr int NK = 4 * NB;                 // MMA steps over the channels
   constexpr bool PRE = !(F32 && NB == 4);    // the next unit's rows fit in registers
-  constexpr int PARTF = NT * (NB * 4 + 1) * 128;  // floats of a partial
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ unsigned sc[PGA_WARPS + 1];
-  __shared__ long long s_join[2][2];  // units [first, last] of the items this CTA shares with others; -1: none
-  __shared__ int s_joinat[2][2];      // their row and item
+  // items that cross warps or CTAs: first unit (-1: none), unit behind the last, row, item. 0..7: left open by that
+  // warp, which began it; 8: begun by an earlier CTA; 9 and 10: shared with earlier and with later CTAs
+  __shared__ int s_item[11][4];
   __shared__ int s_last;
-  float* s_part = reinterpret_cast<float*>(smem_raw);                    // [warps][PARTF]
-  uint2* s_q = reinterpret_cast<uint2*>(s_part + PGA_WARPS * PARTF);     // [warps][NT][NK][3][32]
-  int* s_pre = reinterpret_cast<int*>(s_q + PGA_WARPS * NT * NK * 3 * 32);  // [B + 1]
+  float* s_part = reinterpret_cast<float*>(smem_raw);  // [warps][PARTF]: what a warp adds to an item begun before it
+  char* s_q = smem_raw + PGA_WARPS * PARTF * 4;        // [warps][QBYTES]: q; at the end of a stretch, an item left open
+  float* s_raw = reinterpret_cast<float*>(s_q + PGA_WARPS * Shape::QBYTES);  // [warps][RAWF]: the next item's q
+  int* s_pre = reinterpret_cast<int*>(s_raw + PGA_WARPS * Shape::RAWF);      // [B + 1]
   int* s_len = s_pre + a.B + 1;                                          // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   griddep_launch();
+  if (tid < 11) s_item[tid][0] = -1;
+  __syncthreads();
   griddep_wait();
 
   // units of every row, and their prefix sums
@@ -426,25 +446,43 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
     nh = hc < 0 ? 0 : min(hc, a.rows);
     if (hc != nh && blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_CLAMPED);
   }
-  unsigned base = 0;
-  for (int r0 = 0; r0 < a.B; r0 += PGA_THREADS) {
-    const int r = r0 + tid;
-    int len = r < a.B ? a.lens[r] : 0;
+  int units = 0;
+  if (a.B <= 32) {  // every warp for itself, the same values: no barrier
+    int len = lane < a.B ? a.lens[lane] : 0;
     if (len > cap) {
       len = cap;
-      if (blockIdx.x == 0) raise_status(a.status, ST_CLAMPED);
+      if (blockIdx.x == 0 && warp == 0) raise_status(a.status, ST_CLAMPED);
     }
-    unsigned tot;
-    const unsigned ex = block_exclusive_scan<PGA_THREADS>(len > 0 ? (unsigned)((len + UNIT - 1) / UNIT) : 0u, sc, &tot);
-    if (r < a.B) {
-      s_pre[r] = base + ex;
-      s_len[r] = len;
+    units = len > 0 ? (len + UNIT - 1) / UNIT : 0;
+    if (lane < a.B) s_len[lane] = len;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, units, x);
+      if (lane >= x) units += y;
     }
-    base += tot;
+    if (lane < a.B) s_pre[lane + 1] = units;
+    if (lane == 0) s_pre[0] = 0;
+    units = __shfl_sync(0xffffffffu, units, 31);
+    __syncwarp();
+  } else {
+    for (int r0 = 0; r0 < a.B; r0 += PGA_THREADS) {
+      const int r = r0 + tid;
+      int len = r < a.B ? a.lens[r] : 0;
+      if (len > cap) {
+        len = cap;
+        if (blockIdx.x == 0) raise_status(a.status, ST_CLAMPED);
+      }
+      unsigned tot;
+      const unsigned ex = block_exclusive_scan<PGA_THREADS>(len > 0 ? (unsigned)((len + UNIT - 1) / UNIT) : 0u, sc, &tot);
+      if (r < a.B) {
+        s_pre[r] = units + ex;
+        s_len[r] = len;
+      }
+      units += tot;
+    }
+    if (tid == 0) s_pre[a.B] = units;
+    __syncthreads();
   }
-  if (tid == 0) s_pre[a.B] = base;
-  if (tid < 2) s_join[tid][0] = -1;
-  __syncthreads();
   const int IR = nh * a.NQ;  // items of a row
   const int HR = a.rows * a.G;  // query rows of a request
   // rows without keys: zeros (and minus infinity)
@@ -454,23 +492,29 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
     if (a.lse)
       for (int i = tid; i < nh * a.G; i += PGA_THREADS) a.lse[(size_t)r * HR + i] = -INFINITY;
   }
-  const long long U = (long long)base * IR;
-  const int CE = (int)min((long long)gridDim.x, (U + PGA_WARPS - 1) / PGA_WARPS);  // CTAs with work
+  const int U = units * IR;  // (below 2^31: checked on the host for the largest lengths)
+  const int CE = min((int)gridDim.x, (U + PGA_WARPS - 1) / PGA_WARPS);  // CTAs with work
   if ((int)blockIdx.x >= CE) return;
-  const int NW = CE * PGA_WARPS, wid = blockIdx.x * PGA_WARPS + warp;
-  const long long wlo = U * wid / NW, whi = U * (wid + 1) / NW;
-  const bool lead = wlo == U * ((long long)blockIdx.x * PGA_WARPS) / NW;  // the CTA's first units are this warp's
+  // Warp w's stretch is [first(w), first(w + 1)): U / NW units, one more for the first U % NW
+  const int NW = CE * PGA_WARPS, w0 = blockIdx.x * PGA_WARPS;
+  const int each = U / NW, extra = U - each * NW;
+  auto first_unit = [&](int w) { return w * each + min(w, extra); };
+  auto cta_of = [&](int u) {
+    const int big = extra * (each + 1);
+    return (u < big ? u / (each + 1) : extra + (u - big) / each) / PGA_WARPS;  // (u >= big only if each > 0)
+  };
+  const int wlo = first_unit(w0 + warp), whi = first_unit(w0 + warp + 1);
   const int dh8 = a.dh >> 3;
   const KT* Kp = static_cast<const KT*>(a.K);
   const KT* Vp = static_cast<const KT*>(a.V);
 
-  auto locate = [&](long long u) {
+  auto locate = [&](int u) {
     PagedAt p;
-    p.b = row_of(s_pre, a.B, (int)(u / IR));
+    p.b = row_of(s_pre, a.B, u / IR);
     p.nt = s_pre[p.b + 1] - s_pre[p.b];
-    const long long rem = u - (long long)s_pre[p.b] * IR;
-    p.it = (int)(rem / p.nt);
-    p.t = (int)(rem - (long long)p.it * p.nt);
+    const int rem = u - s_pre[p.b] * IR;
+    p.it = rem / p.nt;
+    p.t = rem - p.it * p.nt;
     return p;
   };
   auto advance = [&](PagedAt& p) {  // (never past the last unit)
@@ -495,16 +539,21 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
     return pg * a.stride_rows + head * a.page + (key - pi * a.page);
   };
 
-  float o[NT][NB][4][4], m[NT][2], l[NT][2];
+  float o[NT][NB][8][2], m[NT], l[NT];  // query row g; channels 64 nb + 16 t + e and + 8 + e; l: this lane's keys
   Chunk<KT> kc[2 * MT][NC], vc[NB][4 * MT];
-  unsigned ok = 0;  // keys g + 8 i of the unit in kc that are not masked
+  unsigned in_k = 0;  // keys of the unit in kc that are not masked
   // Whole pages of 16-key tiles and channels without padding: a tile's rows are
   // consecutive, so a lane's loads are one pointer and constant offsets.
   const bool tiled = a.dh == DH && (a.page & 15) == 0;
 
+  // Elsewhere (a masked tail, small pages, padding) every row has a pointer, and
+  // masked rows read a row of the unit that is not: their scores are masked
+  // and their weights zero; channels past dh repeat the last ones, against zeros
+  // of q, and go to sums that are not stored.
+  auto any_of = [&](int row, unsigned in) { return in ? __shfl_sync(0xffffffffu, row, __ffs(in) - 1) : -1; };
   auto load_k = [&](int row) {
-    if (tiled && __all_sync(0xffffffffu, row >= 0)) {
-      ok = ~0u;
+    in_k = __ballot_sync(0xffffffffu, row >= 0);
+    if (tiled && in_k == ~0u) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const KT* p = Kp + (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + g) * DH + 8 * t4;
@@ -515,18 +564,22 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
         }
       }
     } else {
-      ok = 0;
+      const int any = any_of(row, in_k);
 #pragma unroll
       for (int j = 0; j < 2 * MT; ++j) {
         const int r = __shfl_sync(0xffffffffu, row, g + 8 * j);
-        ok |= r >= 0 ? 1u << j : 0u;
+        const KT* p = Kp + (long long)(r >= 0 ? r : any) * a.dh;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) kc[j][i].load(Kp, r, dh8, t4 + 4 * i);
+        for (int i = 0; i < NC; ++i) {
+          if (any >= 0) kc[j][i].load(p + 8 * min(t4 + 4 * i, dh8 - 1));
+          else kc[j][i].zero();
+        }
       }
     }
   };
   auto load_v = [&](int row, int nb0, int nb1) {
-    if (tiled && __all_sync(0xffffffffu, row >= 0)) {
+    const unsigned in = __ballot_sync(0xffffffffu, row >= 0);
+    if (tiled && in == ~0u) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const KT* p = Vp + (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + 2 * t4) * DH + 8 * g;
@@ -536,23 +589,48 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
           for (int i = 0; i < 4; ++i) vc[nb][4 * mt + i].load(p + ((i & 1) + (i >> 1) * 8) * DH + 64 * nb);
       }
     } else {
+      const int any = any_of(row, in);
 #pragma unroll
       for (int j = 0; j < 4 * MT; ++j) {
         const int r = __shfl_sync(0xffffffffu, row, 2 * t4 + (j & 1) + (j >> 1) * 8);
+        const KT* p = Vp + (long long)(r >= 0 ? r : any) * a.dh;
 #pragma unroll
-        for (int nb = nb0; nb < nb1; ++nb) vc[nb][j].load(Vp, r, dh8, g + 8 * nb);
+        for (int nb = nb0; nb < nb1; ++nb) {
+          if (any >= 0) vc[nb][j].load(p + 8 * min(g + 8 * nb, dh8 - 1));
+          else vc[nb][j].zero();
+        }
       }
     }
   };
-  uint2* q_mine = s_q + warp * NT * NK * 3 * 32 + lane;
+  uint4* q_mine = reinterpret_cast<uint4*>(s_q + warp * Shape::QBYTES) + lane;
+  float* open_mine = reinterpret_cast<float*>(s_q + warp * Shape::QBYTES);
+  float* part_mine = s_part + warp * PARTF;
 
+  float* raw_mine = s_raw + warp * Shape::RAWF;
+  // q of an item on its way to shared memory
+  auto stage_q = [&](const PagedAt& p) {
+    if constexpr (Shape::STAGE) {
+      const int j = p.it / a.NQ, z = p.it - j * a.NQ;
+      const float* qr = a.q + (((size_t)p.b * a.rows + j) * a.G + z * QR) * a.dh;
+      const int rows = min(QR, a.G - z * QR), d4 = a.dh >> 2;
+      for (int r = 0; r < rows; ++r)
+        for (int c = lane; c < d4; c += 32) {
+          const unsigned to = (unsigned)__cvta_generic_to_shared(raw_mine + r * DH + 4 * c);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(qr + r * a.dh + 4 * c) : "memory");
+        }
+    }
+  };
   // q of an item, split, in the lane's own places of shared memory
   auto begin_item = [&](const PagedAt& p) {
     const int j = p.it / a.NQ, z = p.it - j * a.NQ;
+    if constexpr (Shape::STAGE) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = (z * NT + nt) * 8 + g;
-      const float* qr = a.q + (((size_t)p.b * a.rows + j) * a.G + n) * a.dh;
+      const int n = ONE ? 0 : (z * NT + nt) * 8 + g;
+      const float* qr = Shape::STAGE ? raw_mine + (ONE ? 0 : g) * DH : a.q + (((size_t)p.b * a.rows + j) * a.G + n) * a.dh;
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
         const int c = t4 + 4 * (s >> 1);
@@ -561,328 +639,368 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NT>::CTAS)
         uint2 h, mm, ll;
         split3(x.x, x.y, h.x, mm.x, ll.x);
         split3(x.z, x.w, h.y, mm.y, ll.y);
-        uint2* d = q_mine + (nt * NK + s) * 3 * 32;
-        d[0] = h;
-        d[32] = mm;
-        d[64] = ll;
+        uint4* d = q_mine + (nt * NK + s) * AF * 32;
+        if constexpr (ONE) {  // row 0: high, row 8: middle, row 1: low
+          d[0] = g == 0 ? make_uint4(h.x, mm.x, h.y, mm.y) : g == 1 ? make_uint4(ll.x, 0, ll.y, 0) : make_uint4(0, 0, 0, 0);
+        } else {  // rows 0-7: high, rows 8-15: middle, and low in a fragment of its own
+          d[0] = make_uint4(h.x, mm.x, h.y, mm.y);
+          d[32] = make_uint4(0, ll.x, 0, ll.y);
+        }
       }
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+      m[nt] = -INFINITY;
+      l[nt] = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[nt][nb][e][i] = 0.f;
+        for (int e = 0; e < 8; ++e) o[nt][nb][e][0] = o[nt][nb][e][1] = 0.f;
     }
+    __syncwarp();
   };
-  // l summed over the lanes that share its queries
-  auto total_l = [&]() {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
-  };
-  // A partial: per lane its accumulators and (m, l), as 16-byte vectors
-  auto put_part = [&](float4* d) {
+  // The warp's sums of an item
+  auto put_part = [&](float* d) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          d[((nt * NB + nb) * 4 + e) * 32 + lane] = make_float4(o[nt][nb][e][0], o[nt][nb][e][1], o[nt][nb][e][2], o[nt][nb][e][3]);
-      d[(NT * NB * 4 + nt) * 32 + lane] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
-    }
-  };
-  // `from`: how to read them (shared memory, or another CTA's through L2)
-  auto add_part = [&](const float4* d, auto from) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float4 ml = from(d + (NT * NB * 4 + nt) * 32 + lane);
-      const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w};
-      float c1[2], c2[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float mn = fmaxf(m[nt][i], m2[i]), mu = mn == -INFINITY ? 0.f : mn;
-        c1[i] = exp2f(m[nt][i] - mu);
-        c2[i] = exp2f(m2[i] - mu);
-        l[nt][i] = l[nt][i] * c1[i] + l2[i] * c2[i];
-        m[nt][i] = mn;
+      float sum = l[nt];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int n = ONE ? 0 : nt * 8 + g;
+      const bool mine = !ONE || g == 0;
+      if (mine && t4 == 0) {
+        d[QR * DH + n] = m[nt];
+        d[QR * DH + QR + n] = sum;
       }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 v = from(d + ((nt * NB + nb) * 4 + e) * 32 + lane);
-          o[nt][nb][e][0] = o[nt][nb][e][0] * c1[0] + v.x * c2[0];
-          o[nt][nb][e][1] = o[nt][nb][e][1] * c1[1] + v.y * c2[1];
-          o[nt][nb][e][2] = o[nt][nb][e][2] * c1[0] + v.z * c2[0];
-          o[nt][nb][e][3] = o[nt][nb][e][3] * c1[1] + v.w * c2[1];
-        }
-    }
-  };
-  const auto shared = [](const float4* p) { return *p; };
-  const auto global = [](const float4* p) { return __ldcg(p); };
-  auto output = [&](int b, int it) {
-    const int j = it / a.NQ, z = it - j * a.NQ;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int n = (z * NT + nt) * 8 + 2 * t4 + i;
-        if (n >= a.G) continue;
-        const size_t row = ((size_t)b * a.rows + j) * a.G + n;
-        const float inv = l[nt][i] > 0.f || l[nt][i] != l[nt][i] ? 1.f / l[nt][i] : 0.f;  // (NaN stays)
-        if (a.lse && g == 0) a.lse[row] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + log2f(l[nt][i])) * 0.69314718055994531f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if (g + 8 * nb >= dh8) continue;
-          float4* d = reinterpret_cast<float4*>(a.out + row * a.dh + 8 * (g + 8 * nb));
-          d[0] = make_float4(o[nt][nb][0][i] * inv, o[nt][nb][1][i] * inv, o[nt][nb][2][i] * inv, o[nt][nb][3][i] * inv);
-          d[1] = make_float4(o[nt][nb][0][2 + i] * inv, o[nt][nb][1][2 + i] * inv, o[nt][nb][2][2 + i] * inv, o[nt][nb][3][2 + i] * inv);
-        }
-      }
-  };
-
-  bool held = false, started = false;
-  PagedAt cur = {0, 0, 0, 0};
-  if (wlo < whi) {
-    cur = locate(wlo);
-    PagedAt nxt = cur;
-    const int count = (int)(whi - wlo);
-    int row = pool_row(cur);
-    if (PRE) {
-      load_k(row);
-      load_v(row, 0, NB);
-    }
-    if (count > 1) {
-      advance(nxt);
-      if (PRE) row = pool_row(nxt);
-    }
-    started = cur.t == 0;
-    begin_item(cur);
-#pragma unroll 1
-    for (int n = 0; n < count; ++n) {
-      const bool more = n + 1 < count;
-      if (!PRE) load_k(row);
-      // scores of UNIT keys by 8 NT queries
-      float s[NT][MT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float hi[MT][2][4] = {}, lo[MT][4] = {};
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const uint2* qd = q_mine + (nt * NK + k) * 3 * 32;
-          const uint2 q0 = qd[0], q1 = qd[32], q2 = qd[64];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const Chunk<KT>&x = kc[2 * mt][k >> 1], &y = kc[2 * mt + 1][k >> 1];
-            uint32_t f[SPL][4];
-            if constexpr (!F32) {
-              const int w = (k & 1) * 2;
-              f[0][0] = x.word(w);
-              f[0][1] = y.word(w);
-              f[0][2] = x.word(w + 1);
-              f[0][3] = y.word(w + 1);
-            } else {
-              const int e = (k & 1) * 4;
-              split3(__uint_as_float(x.word(e)), __uint_as_float(x.word(e + 1)), f[0][0], f[1][0], f[2][0]);
-              split3(__uint_as_float(y.word(e)), __uint_as_float(y.word(e + 1)), f[0][1], f[1][1], f[2][1]);
-              split3(__uint_as_float(x.word(e + 2)), __uint_as_float(x.word(e + 3)), f[0][2], f[1][2], f[2][2]);
-              split3(__uint_as_float(y.word(e + 2)), __uint_as_float(y.word(e + 3)), f[0][3], f[1][3], f[2][3]);
-            }
-            mma_bf16(lo[mt], f[0], q2.x, q2.y);
-            if constexpr (F32) {
-              mma_bf16(lo[mt], f[2], q0.x, q0.y);
-              mma_bf16(lo[mt], f[1], q1.x, q1.y);
-              mma_bf16(lo[mt], f[1], q0.x, q0.y);
-            }
-            mma_bf16(lo[mt], f[0], q1.x, q1.y);
-            mma_bf16(hi[mt][k & 1], f[0], q0.x, q0.y);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[nt][mt][i] = (ok >> (2 * mt + (i >> 1))) & 1 ? (hi[mt][0][i] + hi[mt][1][i] + lo[mt][i]) * a.scale_log2 : -INFINITY;
-      }
-      if (PRE && more) load_k(row);
-      // running maximum and sum; p in bf16 terms, transposed into B fragments
-      uint32_t pf[NT][MT][3][2];
-      float corr[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[nt][mt][i], s[nt][mt][2 + i]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-          const float mn = fmaxf(m[nt][i], mx), mu = mn == -INFINITY ? 0.f : mn;
-          corr[nt][i] = exp2f(m[nt][i] - mu);
-          m[nt][i] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            s[nt][mt][i] = exp2f(s[nt][mt][i] - mu);
-            s[nt][mt][2 + i] = exp2f(s[nt][mt][2 + i] - mu);
-            sum += s[nt][mt][i] + s[nt][mt][2 + i];
-          }
-          l[nt][i] = l[nt][i] * corr[nt][i] + sum;
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t h, mm, ll;
-            split3(s[nt][mt][2 * hf], s[nt][mt][2 * hf + 1], h, mm, ll);
-            pf[nt][mt][0][hf] = transpose8x8(h);
-            pf[nt][mt][1][hf] = transpose8x8(mm);
-            pf[nt][mt][2][hf] = transpose8x8(ll);
-          }
-      }
-      // o = o corr + V^T p
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        if (!PRE) load_v(row, nb, nb + 1);
+        if constexpr (ONE) {  // row 1's sums belong to row 0
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float c[NT][4] = {};
+          for (int e = 0; e < 8; ++e) {
+            o[nt][nb][e][0] += __shfl_xor_sync(0xffffffffu, o[nt][nb][e][0], 4);
+            o[nt][nb][e][1] += __shfl_xor_sync(0xffffffffu, o[nt][nb][e][1], 4);
+          }
+        }
+        if (mine) {
+          float4* w = reinterpret_cast<float4*>(d + n * DH + 64 * nb + 16 * t4);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const Chunk<KT>* v = vc[nb] + 4 * mt;
-            uint32_t f[SPL][4];
-            if constexpr (!F32) {
-              const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-              f[0][0] = __byte_perm(v[0].word(e >> 1), v[1].word(e >> 1), sel);
-              f[0][1] = __byte_perm(v[0].word(2 + (e >> 1)), v[1].word(2 + (e >> 1)), sel);
-              f[0][2] = __byte_perm(v[2].word(e >> 1), v[3].word(e >> 1), sel);
-              f[0][3] = __byte_perm(v[2].word(2 + (e >> 1)), v[3].word(2 + (e >> 1)), sel);
-            } else {
-              split3(__uint_as_float(v[0].word(e)), __uint_as_float(v[1].word(e)), f[0][0], f[1][0], f[2][0]);
-              split3(__uint_as_float(v[0].word(4 + e)), __uint_as_float(v[1].word(4 + e)), f[0][1], f[1][1], f[2][1]);
-              split3(__uint_as_float(v[2].word(e)), __uint_as_float(v[3].word(e)), f[0][2], f[1][2], f[2][2]);
-              split3(__uint_as_float(v[2].word(4 + e)), __uint_as_float(v[3].word(4 + e)), f[0][3], f[1][3], f[2][3]);
-            }
+          for (int i = 0; i < 4; ++i)
+            w[i] = make_float4(o[nt][nb][(i & 1) * 4][i >> 1], o[nt][nb][(i & 1) * 4 + 1][i >> 1], o[nt][nb][(i & 1) * 4 + 2][i >> 1],
+                               o[nt][nb][(i & 1) * 4 + 3][i >> 1]);
+        }
+      }
+    }
+  };
+  auto divide = [&](size_t row, int c, float top, float sum, const float4& v) {
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // (NaN stays)
+    if (c < a.dh) *reinterpret_cast<float4*>(a.out + row * a.dh + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    if (a.lse && c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  };
+  // n partials, the first at p0 and the others from p1 on, `step` floats apart, added in that order by all warps: into
+  // a partial `dst`, or divided into the outputs of item (b, it). Eight at a time, so that their loads overlap.
+  auto combine = [&](const float* p0, const float* p1, int step, int n, int b, int it, float* dst) {
+    const int j = it / a.NQ, z = it - j * a.NQ;
+    const int gq = min(QR, a.G - z * QR);
+    const size_t row = ((size_t)b * a.rows + j) * a.G + z * QR;
+#pragma unroll 1
+    for (int x = tid; x < gq * (DH / 4); x += PGA_THREADS) {
+      const int qn = x / (DH / 4), c = (x % (DH / 4)) * 4;
+      float top = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int s0 = 0; s0 < n; s0 += 8) {
+        float pm[8], pl[8];
+        float4 pv[8];
+        float mn = top;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t(&pm)[3][2] = pf[nt][mt];
-              mma_bf16(c[nt], f[0], pm[2][0], pm[2][1]);
-              if constexpr (F32) {
-                mma_bf16(c[nt], f[2], pm[0][0], pm[0][1]);
-                mma_bf16(c[nt], f[1], pm[1][0], pm[1][1]);
-                mma_bf16(c[nt], f[1], pm[0][0], pm[0][1]);
+        for (int i = 0; i < 8; ++i) {
+          const int s = s0 + i;
+          const float* p = s == 0 ? p0 : p1 + (size_t)(s - 1) * step;
+          pm[i] = -INFINITY;
+          pl[i] = 0.f;
+          pv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (s < n) {
+            pm[i] = p[QR * DH + qn];
+            pl[i] = p[QR * DH + QR + qn];
+            pv[i] = *reinterpret_cast<const float4*>(p + qn * DH + c);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mn = fmaxf(mn, pm[i]);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        float f = exp2_ftz(top - mu);
+        sum *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        top = mn;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f = exp2_ftz(pm[i] - mu);
+          sum = fmaf(f, pl[i], sum);
+          acc.x = fmaf(f, pv[i].x, acc.x);
+          acc.y = fmaf(f, pv[i].y, acc.y);
+          acc.z = fmaf(f, pv[i].z, acc.z);
+          acc.w = fmaf(f, pv[i].w, acc.w);
+        }
+      }
+      if (dst) {
+        *reinterpret_cast<float4*>(dst + qn * DH + c) = acc;
+        if (c == 0) {
+          dst[QR * DH + qn] = top;
+          dst[QR * DH + QR + qn] = sum;
+        }
+      } else {
+        divide(row + qn, c, top, sum, acc);
+      }
+    }
+  };
+
+  if (wlo < whi) {
+    PagedAt cur = locate(wlo);
+    if (warp == 0 && lane == 0 && cur.t > 0) {
+      s_item[8][0] = wlo - cur.t;
+      s_item[8][1] = wlo - cur.t + cur.nt;
+      s_item[8][2] = cur.b;
+      s_item[8][3] = cur.it;
+    }
+    PagedAt nxt = cur;
+    const int count = whi - wlo;
+    int row = pool_row(cur);
+    bool started = cur.t == 0;
+    stage_q(cur);
+    // (pass -1 only requests the first unit's rows, so the loads stand here once)
+#pragma unroll 1
+    for (int n = PRE ? -1 : 0; n < count; ++n) {
+      const bool more = n + 1 < count, real = !PRE || n >= 0;
+      if (!PRE) load_k(row);
+      if (!PRE && n == 0) {
+        begin_item(cur);
+        if (count > 1) {
+          advance(nxt);
+          if (nxt.t == 0) stage_q(nxt);
+        }
+      }
+      float s[NT][2 * MT][2];  // scores, then weights, of keys 8 j + 2 t and + 1
+      float corr[NT];
+      const unsigned in = in_k >> (2 * t4);
+      if (real) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[2 * MT][4];
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            const uint4* qd = q_mine + (nt * NK + k) * AF * 32;
+            const uint4 qa = qd[0], qb = qd[ONE ? 0 : 32];
+            const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
+#pragma unroll
+            for (int half = 0; half < (F32 ? 2 : 1); ++half) {  // (fp32: fewer fragments at a time)
+              constexpr int JN = F32 ? MT : 2 * MT;
+              uint32_t b0[JN][SPL], b1[JN][SPL];
+#pragma unroll
+              for (int i = 0; i < JN; ++i) {
+                const Chunk<KT>& x = kc[half * JN + i][k >> 1];
+                if constexpr (!F32) {
+                  b0[i][0] = x.word((k & 1) * 2);
+                  b1[i][0] = x.word((k & 1) * 2 + 1);
+                } else {
+                  const int e = (k & 1) * 4;
+                  split3(__uint_as_float(x.word(e)), __uint_as_float(x.word(e + 1)), b0[i][0], b0[i][1], b0[i][2]);
+                  split3(__uint_as_float(x.word(e + 2)), __uint_as_float(x.word(e + 3)), b1[i][0], b1[i][1], b1[i][2]);
+                }
               }
-              mma_bf16(c[nt], f[0], pm[1][0], pm[1][1]);
-              mma_bf16(c[nt], f[0], pm[0][0], pm[0][1]);
+              // products from the smallest on, those of one score apart
+#pragma unroll
+              for (int t = SPL - 1; t >= 0; --t)
+#pragma unroll
+                for (int i = 0; i < JN; ++i) {
+                  if (k == 0 && t == SPL - 1) mma_bf16_first(c[half * JN + i], fa, b0[i][t], b1[i][t]);
+                  else mma_bf16(c[half * JN + i], fa, b0[i][t], b1[i][t]);
+                }
+              if constexpr (!ONE) {
+#pragma unroll
+                for (int i = 0; i < JN; ++i) mma_bf16(c[half * JN + i], fb, b0[i][0], b1[i][0]);
+              }
             }
           }
+#pragma unroll
+          for (int j = 0; j < 2 * MT; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float v = c[j][i] + c[j][2 + i];
+              if constexpr (ONE) v += __shfl_xor_sync(0xffffffffu, v, 4);  // row 1's: rows 0 and 1 get the score
+              s[nt][j][i] = v * a.scale_log2;
+            }
+        }
+        if (__builtin_expect(in_k != ~0u, 0)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[nt][nb][e][i] = fmaf(o[nt][nb][e][i], corr[nt][i & 1], c[nt][i]);
+            for (int j = 0; j < 2 * MT; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (!((in >> (8 * j + i)) & 1)) s[nt][j][i] = -INFINITY;
+        }
+      }
+      if (PRE && more) load_k(row);
+      if (real) {
+        // running maximum and sum; p in bf16 terms: the scores' places are the A fragments' of the second product
+        uint32_t pf[NT][MT][AF][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2 * MT; ++j) mx = fmaxf(mx, fmaxf(s[nt][j][0], s[nt][j][1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[nt], mx), mu = mn == -INFINITY ? 0.f : mn;
+          corr[nt] = exp2_ftz(m[nt] - mu);
+          m[nt] = mn;
+#pragma unroll
+          for (int j = 0; j < 2 * MT; ++j) {
+            const float x = exp2_ftz(s[nt][j][0] - mu), y = exp2_ftz(s[nt][j][1] - mu);
+            sum += x + y;
+            uint32_t h, mm, ll;
+            split3(x, y, h, mm, ll);
+            uint32_t(&f)[AF][4] = pf[nt][j >> 1];
+            if constexpr (ONE) {
+              f[0][(j & 1) * 2] = g == 0 ? h : g == 1 ? ll : 0u;
+              f[0][(j & 1) * 2 + 1] = g == 0 ? mm : 0u;
+            } else {
+              f[0][(j & 1) * 2] = h;
+              f[0][(j & 1) * 2 + 1] = mm;
+              f[AF - 1][(j & 1) * 2] = 0u;
+              f[AF - 1][(j & 1) * 2 + 1] = ll;
+            }
+          }
+          l[nt] = l[nt] * corr[nt] + sum;
+        }
+        // o = o corr + p V
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (!PRE) load_v(row, nb, nb + 1);
+#pragma unroll
+          for (int e0 = 0; e0 < 8; e0 += EN) {
+            float c[NT][EN][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const Chunk<KT>* v = vc[nb] + 4 * mt;
+              uint32_t b0[EN][SPL], b1[EN][SPL];
+#pragma unroll
+              for (int i = 0; i < EN; ++i) {
+                const int e = e0 + i;
+                if constexpr (!F32) {
+                  const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+                  b0[i][0] = __byte_perm(v[0].word(e >> 1), v[1].word(e >> 1), sel);
+                  b1[i][0] = __byte_perm(v[2].word(e >> 1), v[3].word(e >> 1), sel);
+                } else {
+                  split3(__uint_as_float(v[0].word(e)), __uint_as_float(v[1].word(e)), b0[i][0], b0[i][1], b0[i][2]);
+                  split3(__uint_as_float(v[2].word(e)), __uint_as_float(v[3].word(e)), b1[i][0], b1[i][1], b1[i][2]);
+                }
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t(&f)[AF][4] = pf[nt][mt];
+#pragma unroll
+                for (int t = SPL - 1; t >= 0; --t)
+#pragma unroll
+                  for (int i = 0; i < EN; ++i) {
+                    if (mt == 0 && t == SPL - 1) mma_bf16_first(c[nt][i], f[0], b0[i][t], b1[i][t]);
+                    else mma_bf16(c[nt][i], f[0], b0[i][t], b1[i][t]);
+                  }
+                if constexpr (!ONE) {
+#pragma unroll
+                  for (int i = 0; i < EN; ++i) mma_bf16(c[nt][i], f[AF - 1], b0[i][0], b1[i][0]);
+                }
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < EN; ++i) {
+                float(&d)[2] = o[nt][nb][e0 + i];
+                d[0] = fmaf(d[0], corr[nt], c[nt][i][0] + c[nt][i][2]);
+                d[1] = fmaf(d[1], corr[nt], c[nt][i][1] + c[nt][i][3]);
+              }
+          }
         }
       }
       if (PRE && more) load_v(row, 0, NB);
-      const bool ends = cur.t + 1 == cur.nt;
-      if (ends || !more) {
-        total_l();
+      const bool ends = real && cur.t + 1 == cur.nt;
+      if (real && (ends || !more)) {
+        __syncwarp();
+        put_part(started ? open_mine : part_mine);
+        __syncwarp();
         if (started && ends) {
-          output(cur.b, cur.it);
-        } else if (!started && !lead) {
-          put_part(reinterpret_cast<float4*>(s_part + warp * PARTF));
-        } else if (ends) {  // an item that earlier CTAs began ends in the first warp
-          put_part(reinterpret_cast<float4*>(a.part + (size_t)blockIdx.x * 2 * PARTF));
-          if (lane == 0) {
-            s_join[0][0] = wlo + n - cur.t;
-            s_join[0][1] = wlo + n;
-            s_joinat[0][0] = cur.b;
-            s_joinat[0][1] = cur.it;
+          const int j = cur.it / a.NQ, z = cur.it - j * a.NQ, gq = min(QR, a.G - z * QR);
+          const size_t out_row = ((size_t)cur.b * a.rows + j) * a.G + z * QR;
+#pragma unroll 1
+          for (int x = lane; x < gq * (DH / 4); x += 32) {
+            const int qn = x / (DH / 4), c = (x % (DH / 4)) * 4;
+            divide(out_row + qn, c, open_mine[QR * DH + qn], open_mine[QR * DH + QR + qn],
+                   *reinterpret_cast<const float4*>(open_mine + qn * DH + c));
           }
-        } else {
-          held = true;
+          __syncwarp();
+        } else if (started && lane == 0) {
+          s_item[warp][0] = whi - 1 - cur.t;
+          s_item[warp][1] = whi - 1 - cur.t + cur.nt;
+          s_item[warp][2] = cur.b;
+          s_item[warp][3] = cur.it;
         }
       }
       if (more) {
-        cur = nxt;
+        if (real) cur = nxt;
         if (n + 2 < count) advance(nxt);
         if (!PRE) row = pool_row(cur);
         else if (n + 2 < count) row = pool_row(nxt);
-        if (ends) {
-          started = true;
-          begin_item(cur);
-        }
+        if (ends) started = true;
+        if (ends || n < 0) begin_item(cur);
+        if (n + 2 < count && nxt.t == 0) stage_q(nxt);
       }
     }
   }
   __syncthreads();
 
-  // What crosses warps: the item's first warp in this CTA adds the others' partials
-  const long long chi = U * ((long long)(blockIdx.x + 1) * PGA_WARPS) / NW;
-  if (held) {
-    const long long first = whi - 1 - cur.t, end = first + cur.nt;
-    for (int w = warp + 1; w < PGA_WARPS; ++w) {
-      const long long lo = U * (blockIdx.x * PGA_WARPS + w) / NW, hi = U * (blockIdx.x * PGA_WARPS + w + 1) / NW;
-      if (lo >= hi) continue;
-      if (lo >= end) break;
-      add_part(reinterpret_cast<const float4*>(s_part + w * PARTF), shared);
-    }
-    if (started && end <= chi) {
-      output(cur.b, cur.it);
-    } else {
-      const int slot = started ? 1 : 0;
-      put_part(reinterpret_cast<float4*>(a.part + ((size_t)blockIdx.x * 2 + slot) * PARTF));
-      if (lane == 0) {
-        s_join[slot][0] = first;
-        s_join[slot][1] = end - 1;
-        s_joinat[slot][0] = cur.b;
-        s_joinat[slot][1] = cur.it;
-      }
-    }
-  }
-  __threadfence();
-  __syncthreads();
-  // What crosses CTAs: the last to arrive adds the partials of CTAs c0 .. c0 + n - 1
+  // What crosses warps or CTAs, item by item: those of this CTA (0..8), then those shared with other CTAs, by the last
+  // CTA to arrive. Partials are added in the order of their warps, then of their CTAs.
 #pragma unroll 1
-  for (int s = 0; s < 2; ++s) {
-    const long long u0 = s_join[s][0];
-    if (u0 < 0) continue;
-    const int c0 = (int)(((u0 + 1) * NW - 1) / U) / PGA_WARPS;
-    const int n = (int)(((s_join[s][1] + 1) * NW - 1) / U) / PGA_WARPS - c0 + 1;
-    if (tid == 0) {
-      const unsigned old = atomicAdd(a.tick + c0, 1u);
-      s_last = old == (unsigned)(n - 1);
-      if (s_last) a.tick[c0] = 0;
+  for (int i = 0; i < 11; ++i) {
+    int* it = s_item[i];
+    const int begin = it[0], end = it[1];
+    if (begin >= 0) {
+      const float *p0, *p1;
+      float* dst = nullptr;
+      int n, step;
+      if (i < 9) {
+        const int w = i & 7;
+        p0 = i < 8 ? reinterpret_cast<const float*>(s_q + w * Shape::QBYTES) : s_part;
+        p1 = s_part + (w + 1) * PARTF;
+        step = PARTF;
+        n = 1;
+        while (w + n < PGA_WARPS && first_unit(w0 + w + n) < end) ++n;
+        if (i == 8 || end > first_unit(w0 + PGA_WARPS)) {
+          const int shared = i == 8 ? 9 : 10;
+          dst = a.part + ((size_t)blockIdx.x * 2 + shared - 9) * PARTF;
+          if (tid < 4) s_item[shared][tid] = it[tid];
+        }
+      } else {
+        const int c0 = cta_of(begin);
+        n = cta_of(end - 1) - c0 + 1;
+        __syncthreads();
+        if (tid == 0) {
+          const unsigned old = atomicAdd(a.tick + c0, 1u);
+          s_last = old == (unsigned)(n - 1);
+          if (s_last) a.tick[c0] = 0;
+          __threadfence();
+        }
+        __syncthreads();
+        p0 = a.part + ((size_t)c0 * 2 + 1) * PARTF;  // begun in c0, carried on in the next CTAs
+        p1 = a.part + ((size_t)c0 + 1) * 2 * PARTF;
+        step = 2 * PARTF;
+        if (!s_last) n = 0;
+      }
+      if (n > 0) combine(p0, p1, step, n, it[2], it[3], dst);
+    }
+    if (i == 8) {
       __threadfence();
-    }
-    __syncthreads();
-    if (s_last) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[nt][nb][e][i] = 0.f;
-      }
-      for (int p = warp; p < n; p += PGA_WARPS)
-        add_part(reinterpret_cast<const float4*>(a.part + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * PARTF), global);
-      if (warp > 0) put_part(reinterpret_cast<float4*>(s_part + warp * PARTF));
       __syncthreads();
-      if (warp == 0) {
-        for (int w = 1; w < PGA_WARPS && w < n; ++w) add_part(reinterpret_cast<const float4*>(s_part + w * PARTF), shared);
-        output(s_joinat[s][0], s_joinat[s][1]);
-      }
+      if (s_item[9][0] < 0 && s_item[10][0] < 0) return;
     }
-    __syncthreads();
   }
 }
 

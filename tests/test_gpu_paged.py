@@ -116,11 +116,15 @@ def test_long_rows_are_split_and_joined(dtype, hkv, G, n, page):
     check_attn(out, lse, K, V, table, lens, q, 0.125)
 
 
-@pytest.mark.parametrize("B, top", [(300, 40), (1500, 9), (4096, 3), (33, 700)])
-def test_many_rows_of_different_lengths(B, top):
+@pytest.mark.parametrize("B, top, hq, hkv, dh, page, dtype", [
+    (300, 40, 4, 2, 64, 8, "bf16"), (1500, 9, 4, 2, 64, 8, "bf16"), (4096, 3, 4, 2, 64, 8, "bf16"), (33, 700, 4, 2, 64, 8, "bf16"),
+    (40, 900, 3, 3, 128, 16, "bf16"), (60, 500, 8, 2, 128, 32, "bf16"), (24, 700, 24, 2, 128, 16, "bf16"), (20, 900, 4, 2, 256, 16, "bf16"),
+    (20, 900, 3, 3, 256, 16, "f32"), (20, 700, 8, 2, 256, 16, "f32"), (30, 800, 6, 3, 128, 16, "f32"), (33, 600, 3, 3, 64, 16, "f32"),
+    (30, 400, 36, 2, 64, 16, "f32"), (40, 600, 5, 5, 96, 16, "bf16"), (30, 600, 16, 2, 96, 24, "f32")])
+def test_many_rows_of_different_lengths(B, top, hq, hkv, dh, page, dtype):
     lens = [(i * 7919) % (top + 1) for i in range(B)]
-    K, V, table, lens_t = make_cache(lens, 2, 64, 8, BF16, B)
-    q = torch.randn(B, 4, 64, generator=gen(5), device="cuda")
+    K, V, table, lens_t = make_cache(lens, hkv, dh, page, BF16 if dtype == "bf16" else F32, B)
+    q = torch.randn(B, hq, dh, generator=gen(5), device="cuda")
     out, lse, status = run_attn(K, V, table, lens_t, q, 0.125)
     assert status == 0
     check_attn(out, lse, K, V, table, lens_t, q, 0.125)
