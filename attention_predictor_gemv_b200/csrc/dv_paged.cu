@@ -13,46 +13,20 @@ constexpr int CTAS_PER_SM = 2;  // of the attention kernel, at most
 bool dtype_ok(int t) { return t == DV_F32 || t == DV_BF16; }
 int blocks64(int dh) { return dh <= 64 ? 1 : dh <= 128 ? 2 : 4; }
 
-// Shared memory per SM that the attention asks for: its CTAs' own and no more.
-// Its loads in flight live in the rest, the L1 cache: with the largest shared
-// memory (28 KB of L1) they were bound to 4.8 TB/s.
-template <typename K>
-cudaError_t carve_out(K kern, size_t bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const int percent = (int)((bytes * 100 + 228 * 1024 - 1) / (228 * 1024));
-  const auto key = std::make_pair(reinterpret_cast<const void*>(kern), dev);
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, int> set;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = set.find(key);
-  if (it != set.end() && it->second == percent) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, percent > 100 ? 100 : percent);
-  if (e == cudaSuccess) {
-    set[key] = percent;
-    std::lock_guard<std::mutex> lock2(g_carve_mu);
-    g_carve_set[key] = true;  // (launch() leaves it as it is)
-  }
-  return e;
-}
-
 template <typename KT, int NB, int NT>
 cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
   using Shape = PagedShape<KT, NB, NT>;
   constexpr int per_sm = Shape::CTAS, UNIT = Shape::UNIT;
   static_assert(per_sm <= CTAS_PER_SM && Shape::PARTF <= 16 * (Shape::DH + 2), "partial slots");
   a.NQ = (a.G + Shape::QR - 1) / Shape::QR;
-  const size_t smem = PGA_WARPS * (4ull * (Shape::PARTF + Shape::RAWF) + Shape::QBYTES) + 4ull * (2 * a.B + 1);
+  const size_t smem = (size_t)Shape::WARPS * Shape::WARP_BYTES + 4ull * (a.B + 1);
   cudaError_t e = allow_smem(paged_attn_kernel<KT, NB, NT>, smem);
   if (e != cudaSuccess) return e;
   const long long cap = (long long)a.W * a.page;
   const long long most = a.B * ((cap + UNIT - 1) / UNIT) * (long long)a.rows * a.NQ;  // units, at most
-  const long long want = (most + PGA_WARPS - 1) / PGA_WARPS, have = (long long)sm_count() * per_sm;
-  e = carve_out(paged_attn_kernel<KT, NB, NT>, per_sm * (smem + 1024));
-  if (e != cudaSuccess) return e;
+  const long long want = (most + Shape::WARPS - 1) / Shape::WARPS, have = (long long)sm_count() * per_sm;
   return launch_main(paged_attn_kernel<KT, NB, NT>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
-                     dim3(PGA_THREADS), smem, st, a);
+                     dim3(32 * Shape::WARPS), smem, st, a);
 }
 
 template <typename KT>

@@ -334,8 +334,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_token_kernel(PagedTokenArgs 
 // staging and no barrier in the loop; the next unit's K is requested once the
 // scores of this one are formed, its V once this one's is used.
 // ----------------------------------------------------------------------------
-constexpr int PGA_WARPS = 8;
-constexpr int PGA_THREADS = PGA_WARPS * 32;
+constexpr int PGA_MAX_WARPS = 8;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -364,75 +363,74 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& 
   l = bf16_pair(x1 - __uint_as_float(m << 16), y1 - __uint_as_float(m & 0xffff0000u));
 }
 
-// A stretch's place: row b, item it within the row, unit t of nt.
-struct PagedAt {
-  int b, it, t, nt;
-};
+__device__ __forceinline__ uint32_t word_of(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
-// Eight channels of a cache row in registers.
-template <typename KT>
-struct Chunk {
-  static constexpr int N = sizeof(KT) / 2;
-  uint4 v[N];
-  __device__ __forceinline__ void load(const KT* p) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ uint32_t word(int i) const {  // i-th 32-bit word
-    const uint4& u = v[i >> 2];
-    return (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
-  }
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest group have landed, the whole warp's
+__device__ __forceinline__ void copies_wait_all_but_one() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  __syncwarp();
+}
+
+// A stretch's place: row b of `len` keys, item it within the row, unit t of nt.
+struct PagedAt {
+  int b, it, t, nt, len;
 };
 
 // Shape of a kernel for NB blocks of 64 channels and NT groups of 8 query heads
-// (NT = 0: one query head, its bf16 terms in three rows of one group):
-// 16-key tiles in a unit, CTAs per SM, query rows, floats of a partial
-// ([QR][DH] sums, then QR maxima and QR weight sums), bytes of q a warp keeps.
+// (NT = 0: one query head, its bf16 terms in three rows of one group): warps of
+// a CTA, 16-key tiles in a unit, CTAs per SM, query rows, floats of a partial
+// ([QR][DH] sums, then QR maxima and QR weight sums), and shared memory per
+// warp: K and V rows of a unit, a partial, the next item's q.
 template <typename KT, int NB, int NT>
 struct PagedShape {
-  static constexpr int BYTES = sizeof(KT) * NB;  // a tile's K row bytes / 64
-  static constexpr int MT = BYTES <= 4 && NT <= 1 ? 2 : 1;
-  static constexpr int CTAS = BYTES == 2 && NT <= 1 ? 2 : 1;
-  static constexpr int UNIT = 16 * MT;
   static constexpr int DH = 64 * NB;
+  static constexpr int ROW = DH * sizeof(KT);  // bytes
+  static constexpr int PITCH = ROW + 16;       // of rows in shared memory: 16-byte pieces of neighbours in other banks
+  static constexpr int WARPS = ROW <= 512 ? 8 : 4;
+  static constexpr int MT = ROW <= 256 && NT <= 1 ? 2 : 1;
+  static constexpr int UNIT = 16 * MT;
+  static constexpr int CTAS = ROW == 128 && NT <= 1 ? 2 : 1;
   static constexpr int QR = NT == 0 ? 1 : 8 * NT;
   static constexpr int PARTF = (QR * (DH + 2) + 3) & ~3;
-  static constexpr int QFRAGS = NT == 0 ? 1 : 2 * NT;
-  static constexpr int QBYTES = QFRAGS * 4 * NB * 32 * 16;
   static constexpr bool STAGE = NT == 0 || (NT == 1 && NB <= 2);  // the next item's q is copied ahead
   static constexpr int RAWF = STAGE ? QR * DH : 0;
-  static_assert(QBYTES >= 4 * PARTF, "a warp's last partial takes the place of its q");
+  static constexpr int SLOT = UNIT * PITCH;
+  static constexpr int WARP_BYTES = 2 * SLOT + 4 * (PARTF + RAWF);
+  static_assert(2 * SLOT >= 4 * PARTF, "an item left open at the end of a stretch takes the place of K and V");
+  static_assert(WARPS * WARP_BYTES + 4 * (PAGED_MAX_ROWS + 1) + 1024 <= 227 * 1024, "shared memory");
 };
 
 template <typename KT, int NB, int NTQ>
-__global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
+__global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShape<KT, NB, NTQ>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
   using Shape = PagedShape<KT, NB, NTQ>;
   constexpr bool F32 = sizeof(KT) == 4, ONE = NTQ == 0;
   constexpr int NT = ONE ? 1 : NTQ;
   constexpr int MT = Shape::MT, UNIT = Shape::UNIT, DH = Shape::DH, QR = Shape::QR, PARTF = Shape::PARTF;
-  constexpr int SPL = F32 ? 3 : 1;           // bf16 terms of a cache element
-  constexpr int AF = ONE ? 1 : 2;            // A fragments that hold the terms of q, and of p
+  constexpr int WARPS = Shape::WARPS, THREADS = 32 * WARPS, ROW = Shape::ROW, PITCH = Shape::PITCH;
+  constexpr int SPL = F32 ? 3 : 1;  // bf16 terms of a cache element
+  constexpr int AF = ONE ? 1 : 2;   // A fragments that hold the terms of q, and of p
+  constexpr int NK = 4 * NB;        // MMA steps over the channels
   constexpr int EN = F32 || NT > 1 ? 2 : 4;  // channel tiles whose products run side by side
-  constexpr int NC = 2 * NB;                 // K chunks a lane holds per row
-  constexpr int NK = 4 * NB;                 // MMA steps over the channels
-  constexpr bool PRE = !(F32 && NB == 4);    // the next unit's rows fit in registers
   extern __shared__ __align__(16) char smem_raw[];
-  __shared__ unsigned sc[PGA_WARPS + 1];
+  __shared__ unsigned sc[WARPS + 1];
   // items that cross warps or CTAs: first unit (-1: none), unit behind the last, row, item. 0..7: left open by that
   // warp, which began it; 8: begun by an earlier CTA; 9 and 10: shared with earlier and with later CTAs
   __shared__ int s_item[11][4];
   __shared__ int s_last;
-  float* s_part = reinterpret_cast<float*>(smem_raw);  // [warps][PARTF]: what a warp adds to an item begun before it
-  char* s_q = smem_raw + PGA_WARPS * PARTF * 4;        // [warps][QBYTES]: q; at the end of a stretch, an item left open
-  float* s_raw = reinterpret_cast<float*>(s_q + PGA_WARPS * Shape::QBYTES);  // [warps][RAWF]: the next item's q
-  int* s_pre = reinterpret_cast<int*>(s_raw + PGA_WARPS * Shape::RAWF);      // [B + 1]
-  int* s_len = s_pre + a.B + 1;                                          // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  int* s_pre = reinterpret_cast<int*>(smem_raw + WARPS * Shape::WARP_BYTES);  // [B + 1]
+  // per warp: K rows, V rows (at the end of the stretch an item left open), what it adds to an item begun before it, q
+  char* mine = smem_raw + warp * Shape::WARP_BYTES;
+  auto part_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES + 2 * Shape::SLOT); };
+  auto open_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES); };
   griddep_launch();
   if (tid < 11) s_item[tid][0] = -1;
   __syncthreads();
@@ -446,15 +444,12 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     nh = hc < 0 ? 0 : min(hc, a.rows);
     if (hc != nh && blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_CLAMPED);
   }
+  const int HR = a.rows * a.G;  // query rows of a request
   int units = 0;
   if (a.B <= 32) {  // every warp for itself, the same values: no barrier
-    int len = lane < a.B ? a.lens[lane] : 0;
-    if (len > cap) {
-      len = cap;
-      if (blockIdx.x == 0 && warp == 0) raise_status(a.status, ST_CLAMPED);
-    }
-    units = len > 0 ? (len + UNIT - 1) / UNIT : 0;
-    if (lane < a.B) s_len[lane] = len;
+    const int len = lane < a.B ? a.lens[lane] : 0;
+    if (len > cap && blockIdx.x == 0 && warp == 0) raise_status(a.status, ST_CLAMPED);
+    units = len > 0 ? (min(len, cap) + UNIT - 1) / UNIT : 0;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, units, x);
@@ -465,53 +460,45 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     units = __shfl_sync(0xffffffffu, units, 31);
     __syncwarp();
   } else {
-    for (int r0 = 0; r0 < a.B; r0 += PGA_THREADS) {
+    for (int r0 = 0; r0 < a.B; r0 += THREADS) {
       const int r = r0 + tid;
-      int len = r < a.B ? a.lens[r] : 0;
-      if (len > cap) {
-        len = cap;
-        if (blockIdx.x == 0) raise_status(a.status, ST_CLAMPED);
-      }
+      const int len = r < a.B ? a.lens[r] : 0;
+      if (len > cap && blockIdx.x == 0) raise_status(a.status, ST_CLAMPED);
       unsigned tot;
-      const unsigned ex = block_exclusive_scan<PGA_THREADS>(len > 0 ? (unsigned)((len + UNIT - 1) / UNIT) : 0u, sc, &tot);
-      if (r < a.B) {
-        s_pre[r] = units + ex;
-        s_len[r] = len;
-      }
+      const unsigned ex = block_exclusive_scan<THREADS>(len > 0 ? (unsigned)((min(len, cap) + UNIT - 1) / UNIT) : 0u, sc, &tot);
+      if (r < a.B) s_pre[r] = units + ex;
       units += tot;
     }
     if (tid == 0) s_pre[a.B] = units;
     __syncthreads();
   }
-  const int IR = nh * a.NQ;  // items of a row
-  const int HR = a.rows * a.G;  // query rows of a request
   // rows without keys: zeros (and minus infinity)
   for (int r = blockIdx.x; r < a.B; r += gridDim.x) {
-    if (s_len[r] > 0) continue;
-    for (int i = tid; i < nh * a.G * a.dh; i += PGA_THREADS) a.out[(size_t)r * HR * a.dh + i] = 0.f;
+    if (s_pre[r + 1] > s_pre[r]) continue;
+    for (int i = tid; i < nh * a.G * a.dh; i += THREADS) a.out[(size_t)r * HR * a.dh + i] = 0.f;
     if (a.lse)
-      for (int i = tid; i < nh * a.G; i += PGA_THREADS) a.lse[(size_t)r * HR + i] = -INFINITY;
+      for (int i = tid; i < nh * a.G; i += THREADS) a.lse[(size_t)r * HR + i] = -INFINITY;
   }
-  const int U = units * IR;  // (below 2^31: checked on the host for the largest lengths)
-  const int CE = min((int)gridDim.x, (U + PGA_WARPS - 1) / PGA_WARPS);  // CTAs with work
+  const int IR = nh * a.NQ;     // items of a row
+  const int U = units * IR;     // (below 2^31: checked on the host for the largest lengths)
+  const int CE = min((int)gridDim.x, (U + WARPS - 1) / WARPS);  // CTAs with work
   if ((int)blockIdx.x >= CE) return;
   // Warp w's stretch is [first(w), first(w + 1)): U / NW units, one more for the first U % NW
-  const int NW = CE * PGA_WARPS, w0 = blockIdx.x * PGA_WARPS;
+  const int NW = CE * WARPS, w0 = blockIdx.x * WARPS;
   const int each = U / NW, extra = U - each * NW;
   auto first_unit = [&](int w) { return w * each + min(w, extra); };
   auto cta_of = [&](int u) {
     const int big = extra * (each + 1);
-    return (u < big ? u / (each + 1) : extra + (u - big) / each) / PGA_WARPS;  // (u >= big only if each > 0)
+    return (u < big ? u / (each + 1) : extra + (u - big) / each) / WARPS;  // (u >= big only if each > 0)
   };
   const int wlo = first_unit(w0 + warp), whi = first_unit(w0 + warp + 1);
-  const int dh8 = a.dh >> 3;
-  const KT* Kp = static_cast<const KT*>(a.K);
-  const KT* Vp = static_cast<const KT*>(a.V);
+  const int row_bytes = a.dh * (int)sizeof(KT);
 
   auto locate = [&](int u) {
     PagedAt p;
     p.b = row_of(s_pre, a.B, u / IR);
     p.nt = s_pre[p.b + 1] - s_pre[p.b];
+    p.len = min(a.lens[p.b], cap);
     const int rem = u - s_pre[p.b] * IR;
     p.it = rem / p.nt;
     p.t = rem - p.it * p.nt;
@@ -523,12 +510,13 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     if (++p.it < IR) return;
     p.it = 0;
     do { ++p.b; } while ((p.nt = s_pre[p.b + 1] - s_pre[p.b]) == 0);
+    p.len = min(a.lens[p.b], cap);
   };
   // The pool row of key `lane` of a unit (of 16: both halves of the warp alike), -1 where masked
   auto pool_row = [&](const PagedAt& p) {
     const int key = p.t * UNIT + (lane & (UNIT - 1));
-    if (key >= s_len[p.b]) return -1;
-    const int j = p.it / a.NQ;
+    if (key >= p.len) return -1;
+    const int j = a.NQ == 1 ? p.it : p.it / a.NQ;
     const int head = a.head_idx ? a.head_idx[j] : j;
     const int pi = a.page_shift >= 0 ? key >> a.page_shift : key / a.page;
     const int pg = a.table[(size_t)p.b * a.W + pi];
@@ -539,74 +527,41 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     return pg * a.stride_rows + head * a.page + (key - pi * a.page);
   };
 
-  float o[NT][NB][8][2], m[NT], l[NT];  // query row g; channels 64 nb + 16 t + e and + 8 + e; l: this lane's keys
-  Chunk<KT> kc[2 * MT][NC], vc[NB][4 * MT];
-  unsigned in_k = 0;  // keys of the unit in kc that are not masked
-  // Whole pages of 16-key tiles and channels without padding: a tile's rows are
-  // consecutive, so a lane's loads are one pointer and constant offsets.
+  // A unit's rows of K or V on their way to the warp's slot, 16 bytes a lane, whole rows side by side. Where pages
+  // hold whole 16-key tiles and rows have no padding, a tile's rows are consecutive: one pointer and constant
+  // offsets. Masked rows and channels past dh become zeros.
+  constexpr int CPR = ROW / 16 < 32 ? ROW / 16 : 32, RPI = 32 / CPR;  // lanes on a row, rows of one request
+  const uint32_t slot_at = (uint32_t)__cvta_generic_to_shared(mine) + (lane / CPR) * PITCH + (lane % CPR) * 16;
   const bool tiled = a.dh == DH && (a.page & 15) == 0;
-
-  // Elsewhere (a masked tail, small pages, padding) every row has a pointer, and
-  // masked rows read a row of the unit that is not: their scores are masked
-  // and their weights zero; channels past dh repeat the last ones, against zeros
-  // of q, and go to sums that are not stored.
-  auto any_of = [&](int row, unsigned in) { return in ? __shfl_sync(0xffffffffu, row, __ffs(in) - 1) : -1; };
-  auto load_k = [&](int row) {
-    in_k = __ballot_sync(0xffffffffu, row >= 0);
-    if (tiled && in_k == ~0u) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const KT* p = Kp + (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + g) * DH + 8 * t4;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          kc[2 * mt][i].load(p + 32 * i);
-          kc[2 * mt + 1][i].load(p + 8 * DH + 32 * i);
-        }
-      }
-    } else {
-      const int any = any_of(row, in_k);
-#pragma unroll
-      for (int j = 0; j < 2 * MT; ++j) {
-        const int r = __shfl_sync(0xffffffffu, row, g + 8 * j);
-        const KT* p = Kp + (long long)(r >= 0 ? r : any) * a.dh;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          if (any >= 0) kc[j][i].load(p + 8 * min(t4 + 4 * i, dh8 - 1));
-          else kc[j][i].zero();
-        }
-      }
-    }
-  };
-  auto load_v = [&](int row, int nb0, int nb1) {
-    const unsigned in = __ballot_sync(0xffffffffu, row >= 0);
+  auto request = [&](const void* pool, uint32_t slot, int row, unsigned in) {
     if (tiled && in == ~0u) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const KT* p = Vp + (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + 2 * t4) * DH + 8 * g;
+        const char* p = static_cast<const char*>(pool) +
+                        (long long)(__shfl_sync(0xffffffffu, row, 16 * mt) + lane / CPR) * ROW + (lane % CPR) * 16;
 #pragma unroll
-        for (int nb = nb0; nb < nb1; ++nb)
+        for (int i = 0; i < 16 / RPI; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vc[nb][4 * mt + i].load(p + ((i & 1) + (i >> 1) * 8) * DH + 64 * nb);
+          for (int c = 0; c < ROW; c += CPR * 16)
+            copy16(slot + (16 * mt + i * RPI) * PITCH + c, p + i * RPI * ROW + c);
       }
     } else {
-      const int any = any_of(row, in);
 #pragma unroll
-      for (int j = 0; j < 4 * MT; ++j) {
-        const int r = __shfl_sync(0xffffffffu, row, 2 * t4 + (j & 1) + (j >> 1) * 8);
-        const KT* p = Vp + (long long)(r >= 0 ? r : any) * a.dh;
+      for (int i = 0; i < UNIT / RPI; ++i) {
+        const int r = __shfl_sync(0xffffffffu, row, i * RPI + lane / CPR);
 #pragma unroll
-        for (int nb = nb0; nb < nb1; ++nb) {
-          if (any >= 0) vc[nb][j].load(p + 8 * min(g + 8 * nb, dh8 - 1));
-          else vc[nb][j].zero();
+        for (int c = 0; c < ROW; c += CPR * 16) {
+          const int at = (lane % CPR) * 16 + c;
+          const bool on = r >= 0 && at < row_bytes;
+          copy16_or_zero(slot + i * RPI * PITCH + c, static_cast<const char*>(pool) + (on ? (long long)r * row_bytes + at : 0), on);
         }
       }
     }
   };
-  uint4* q_mine = reinterpret_cast<uint4*>(s_q + warp * Shape::QBYTES) + lane;
-  float* open_mine = reinterpret_cast<float*>(s_q + warp * Shape::QBYTES);
-  float* part_mine = s_part + warp * PARTF;
 
-  float* raw_mine = s_raw + warp * Shape::RAWF;
+  float o[NT][NB][8][2], m[NT], l[NT];  // query row g; l: this lane's keys
+  uint32_t qa[NT][NK][4], ql[ONE ? 1 : NT][NK][2];
+  float* raw_mine = part_of(warp) + PARTF;
   // q of an item on its way to shared memory
   auto stage_q = [&](const PagedAt& p) {
     if constexpr (Shape::STAGE) {
@@ -614,37 +569,40 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
       const float* qr = a.q + (((size_t)p.b * a.rows + j) * a.G + z * QR) * a.dh;
       const int rows = min(QR, a.G - z * QR), d4 = a.dh >> 2;
       for (int r = 0; r < rows; ++r)
-        for (int c = lane; c < d4; c += 32) {
-          const unsigned to = (unsigned)__cvta_generic_to_shared(raw_mine + r * DH + 4 * c);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(qr + r * a.dh + 4 * c) : "memory");
-        }
+        for (int c = lane; c < d4; c += 32)
+          copy16((uint32_t)__cvta_generic_to_shared(raw_mine + r * DH + 4 * c), qr + r * a.dh + 4 * c);
     }
   };
-  // q of an item, split, in the lane's own places of shared memory
+  // q of an item as A fragments: rows 0-7 its high terms, rows 8-15 the middle ones, and the low ones in rows 8-15 of
+  // another; of one query row 0 is high, row 8 middle, row 1 low. An MMA step takes from lane t four channels that K's
+  // fragments have there: half of the 16 bytes (bf16) or the 16 bytes (fp32) that it reads, pieces 2 t and 2 t + 1 of
+  // every 128 bytes of the row.
   auto begin_item = [&](const PagedAt& p) {
     const int j = p.it / a.NQ, z = p.it - j * a.NQ;
-    if constexpr (Shape::STAGE) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();
-    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int n = ONE ? 0 : (z * NT + nt) * 8 + g;
       const float* qr = Shape::STAGE ? raw_mine + (ONE ? 0 : g) * DH : a.q + (((size_t)p.b * a.rows + j) * a.G + n) * a.dh;
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
-        const int c = t4 + 4 * (s >> 1);
+        const int c = F32 ? 32 * (s >> 1) + 8 * t4 + 4 * (s & 1) : 64 * (s >> 2) + 16 * t4 + 4 * (s & 3);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n < a.G && c < dh8) x = *reinterpret_cast<const float4*>(qr + 8 * c + 4 * (s & 1));
+        if (n < a.G && c < a.dh) x = *reinterpret_cast<const float4*>(qr + c);
         uint2 h, mm, ll;
         split3(x.x, x.y, h.x, mm.x, ll.x);
         split3(x.z, x.w, h.y, mm.y, ll.y);
-        uint4* d = q_mine + (nt * NK + s) * AF * 32;
-        if constexpr (ONE) {  // row 0: high, row 8: middle, row 1: low
-          d[0] = g == 0 ? make_uint4(h.x, mm.x, h.y, mm.y) : g == 1 ? make_uint4(ll.x, 0, ll.y, 0) : make_uint4(0, 0, 0, 0);
-        } else {  // rows 0-7: high, rows 8-15: middle, and low in a fragment of its own
-          d[0] = make_uint4(h.x, mm.x, h.y, mm.y);
-          d[32] = make_uint4(0, ll.x, 0, ll.y);
+        if constexpr (ONE) {
+          qa[nt][s][0] = g == 0 ? h.x : g == 1 ? ll.x : 0u;
+          qa[nt][s][1] = g == 0 ? mm.x : 0u;
+          qa[nt][s][2] = g == 0 ? h.y : g == 1 ? ll.y : 0u;
+          qa[nt][s][3] = g == 0 ? mm.y : 0u;
+        } else {
+          qa[nt][s][0] = h.x;
+          qa[nt][s][1] = mm.x;
+          qa[nt][s][2] = h.y;
+          qa[nt][s][3] = mm.y;
+          ql[nt][s][0] = ll.x;
+          ql[nt][s][1] = ll.y;
         }
       }
       m[nt] = -INFINITY;
@@ -656,42 +614,60 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     }
     __syncwarp();
   };
-  // The warp's sums of an item
-  auto put_part = [&](float* d) {
+  // The warp's sums complete: l over the lanes of a query, one query's low terms (row 1) added to row 0
+  auto finish = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float sum = l[nt];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int n = ONE ? 0 : nt * 8 + g;
-      const bool mine = !ONE || g == 0;
-      if (mine && t4 == 0) {
-        d[QR * DH + n] = m[nt];
-        d[QR * DH + QR + n] = sum;
-      }
+      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
+      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
+      if constexpr (ONE) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if constexpr (ONE) {  // row 1's sums belong to row 0
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            o[nt][nb][e][0] += __shfl_xor_sync(0xffffffffu, o[nt][nb][e][0], 4);
-            o[nt][nb][e][1] += __shfl_xor_sync(0xffffffffu, o[nt][nb][e][1], 4);
-          }
-        }
-        if (mine) {
-          float4* w = reinterpret_cast<float4*>(d + n * DH + 64 * nb + 16 * t4);
+          for (int e = 0; e < 8; ++e)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = make_float4(o[nt][nb][(i & 1) * 4][i >> 1], o[nt][nb][(i & 1) * 4 + 1][i >> 1], o[nt][nb][(i & 1) * 4 + 2][i >> 1],
-                               o[nt][nb][(i & 1) * 4 + 3][i >> 1]);
-        }
+            for (int i = 0; i < 2; ++i) o[nt][nb][e][i] += __shfl_xor_sync(0xffffffffu, o[nt][nb][e][i], 4);
       }
     }
   };
-  auto divide = [&](size_t row, int c, float top, float sum, const float4& v) {
-    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // (NaN stays)
-    if (c < a.dh) *reinterpret_cast<float4*>(a.out + row * a.dh + c) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-    if (a.lse && c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  // Row g of group nt times f, `dh` channels, to d. Tile e of block nb holds channels 64 nb + 8 (2 t + i) + e (bf16) or
+  // 64 nb + 32 (e / 4) + 4 (2 t + i) + e % 4 (fp32: a lane's 16 bytes of a V row are four channels).
+  auto store_row = [&](int nt, float* d, int dh, float f) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = 64 * nb + (F32 ? 32 * h + 8 * t4 + 4 * i : 16 * t4 + 8 * i + 4 * h);
+          const float(*v)[2] = o[nt][nb] + 4 * h;
+          if (c < dh) *reinterpret_cast<float4*>(d + c) = make_float4(v[0][i] * f, v[1][i] * f, v[2][i] * f, v[3][i] * f);
+        }
+  };
+  auto put_part = [&](float* d) {
+    if (ONE && g > 0) return;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = ONE ? 0 : nt * 8 + g;
+      if (t4 == 0) {
+        d[QR * DH + n] = m[nt];
+        d[QR * DH + QR + n] = l[nt];
+      }
+      store_row(nt, d + n * DH, DH, 1.f);
+    }
+  };
+  const auto inverse = [](float sum) { return sum > 0.f || sum != sum ? 1.f / sum : 0.f; };  // (NaN stays)
+  const auto log_sum = [](float top, float sum) { return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f; };
+  auto output = [&](const PagedAt& p) {
+    const int j = p.it / a.NQ, z = p.it - j * a.NQ;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = z * QR + (ONE ? 0 : nt * 8 + g);
+      if (ONE ? g > 0 : n >= a.G) continue;
+      const size_t row = ((size_t)p.b * a.rows + j) * a.G + n;
+      store_row(nt, a.out + row * a.dh, a.dh, inverse(l[nt]));
+      if (a.lse && t4 == 0) a.lse[row] = log_sum(m[nt], l[nt]);
+    }
   };
   // n partials, the first at p0 and the others from p1 on, `step` floats apart, added in that order by all warps: into
   // a partial `dst`, or divided into the outputs of item (b, it). Eight at a time, so that their loads overlap.
@@ -700,7 +676,7 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     const int gq = min(QR, a.G - z * QR);
     const size_t row = ((size_t)b * a.rows + j) * a.G + z * QR;
 #pragma unroll 1
-    for (int x = tid; x < gq * (DH / 4); x += PGA_THREADS) {
+    for (int x = tid; x < gq * (DH / 4); x += THREADS) {
       const int qn = x / (DH / 4), c = (x % (DH / 4)) * 4;
       float top = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -746,7 +722,10 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
           dst[QR * DH + QR + qn] = sum;
         }
       } else {
-        divide(row + qn, c, top, sum, acc);
+        const float f = inverse(sum);
+        if (c < a.dh)
+          *reinterpret_cast<float4*>(a.out + (row + qn) * a.dh + c) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        if (a.lse && c == 0) a.lse[row + qn] = log_sum(top, sum);
       }
     }
   };
@@ -762,135 +741,151 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
     PagedAt nxt = cur;
     const int count = whi - wlo;
     int row = pool_row(cur);
-    bool started = cur.t == 0;
+    unsigned in = __ballot_sync(0xffffffffu, row >= 0);
     stage_q(cur);
-    // (pass -1 only requests the first unit's rows, so the loads stand here once)
+    request(a.K, slot_at, row, in);
+    copies_commit();
+    request(a.V, slot_at + Shape::SLOT, row, in);
+    copies_commit();
+    if (count > 1) {
+      advance(nxt);
+      row = pool_row(nxt);
+    }
+    bool started = cur.t == 0, fresh = true;
 #pragma unroll 1
-    for (int n = PRE ? -1 : 0; n < count; ++n) {
-      const bool more = n + 1 < count, real = !PRE || n >= 0;
-      if (!PRE) load_k(row);
-      if (!PRE && n == 0) {
-        begin_item(cur);
-        if (count > 1) {
-          advance(nxt);
-          if (nxt.t == 0) stage_q(nxt);
-        }
-      }
+    for (int n = 0; n < count; ++n) {
+      const bool more = n + 1 < count;
+      copies_wait_all_but_one();  // this unit's K, and q
+      if (fresh) begin_item(cur);
+      if (more && nxt.t == 0) stage_q(nxt);  // (lands with the next unit's K)
+      // scores of UNIT keys by QR queries
       float s[NT][2 * MT][2];  // scores, then weights, of keys 8 j + 2 t and + 1
-      float corr[NT];
-      const unsigned in = in_k >> (2 * t4);
-      if (real) {
+      {
+        float c[NT][2 * MT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float c[2 * MT][4];
+        for (int k = 0; k < NK; k += F32 ? 1 : 2) {
+          // 16 bytes of a K row: eight channels (two steps), fp32 four (one)
+          uint32_t b0[2 * MT][F32 ? SPL : 2], b1[2 * MT][F32 ? SPL : 2];
 #pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            const uint4* qd = q_mine + (nt * NK + k) * AF * 32;
-            const uint4 qa = qd[0], qb = qd[ONE ? 0 : 32];
-            const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
+          for (int j = 0; j < 2 * MT; ++j) {
+            const int piece = F32 ? k : k >> 1;
+            const uint4 x = *reinterpret_cast<const uint4*>(mine + (8 * j + g) * PITCH + (piece >> 1) * 128 + t4 * 32 + (piece & 1) * 16);
+            if constexpr (!F32) {
+              b0[j][0] = x.x;
+              b1[j][0] = x.y;
+              b0[j][1] = x.z;
+              b1[j][1] = x.w;
+            } else {
+              split3(__uint_as_float(x.x), __uint_as_float(x.y), b0[j][0], b0[j][1], b0[j][2]);
+              split3(__uint_as_float(x.z), __uint_as_float(x.w), b1[j][0], b1[j][1], b1[j][2]);
+            }
+          }
 #pragma unroll
-            for (int half = 0; half < (F32 ? 2 : 1); ++half) {  // (fp32: fewer fragments at a time)
-              constexpr int JN = F32 ? MT : 2 * MT;
-              uint32_t b0[JN][SPL], b1[JN][SPL];
+          for (int h = 0; h < (F32 ? 1 : 2); ++h)
 #pragma unroll
-              for (int i = 0; i < JN; ++i) {
-                const Chunk<KT>& x = kc[half * JN + i][k >> 1];
-                if constexpr (!F32) {
-                  b0[i][0] = x.word((k & 1) * 2);
-                  b1[i][0] = x.word((k & 1) * 2 + 1);
-                } else {
-                  const int e = (k & 1) * 4;
-                  split3(__uint_as_float(x.word(e)), __uint_as_float(x.word(e + 1)), b0[i][0], b0[i][1], b0[i][2]);
-                  split3(__uint_as_float(x.word(e + 2)), __uint_as_float(x.word(e + 3)), b1[i][0], b1[i][1], b1[i][2]);
-                }
-              }
+            for (int nt = 0; nt < NT; ++nt) {
               // products from the smallest on, those of one score apart
 #pragma unroll
               for (int t = SPL - 1; t >= 0; --t)
 #pragma unroll
-                for (int i = 0; i < JN; ++i) {
-                  if (k == 0 && t == SPL - 1) mma_bf16_first(c[half * JN + i], fa, b0[i][t], b1[i][t]);
-                  else mma_bf16(c[half * JN + i], fa, b0[i][t], b1[i][t]);
+                for (int j = 0; j < 2 * MT; ++j) {
+                  if (k + h == 0 && t == SPL - 1) mma_bf16_first(c[nt][j], qa[nt][k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
+                  else mma_bf16(c[nt][j], qa[nt][k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
                 }
               if constexpr (!ONE) {
+                const uint32_t low[4] = {0u, ql[nt][k + h][0], 0u, ql[nt][k + h][1]};
 #pragma unroll
-                for (int i = 0; i < JN; ++i) mma_bf16(c[half * JN + i], fb, b0[i][0], b1[i][0]);
+                for (int j = 0; j < 2 * MT; ++j) mma_bf16(c[nt][j], low, b0[j][F32 ? 0 : h], b1[j][F32 ? 0 : h]);
               }
             }
-          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2 * MT; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float v = c[j][i] + c[j][2 + i];
+              float v = c[nt][j][i] + c[nt][j][2 + i];
               if constexpr (ONE) v += __shfl_xor_sync(0xffffffffu, v, 4);  // row 1's: rows 0 and 1 get the score
               s[nt][j][i] = v * a.scale_log2;
             }
-        }
-        if (__builtin_expect(in_k != ~0u, 0)) {
+        if (in != ~0u) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2 * MT; ++j)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (!((in >> (8 * j + i)) & 1)) s[nt][j][i] = -INFINITY;
+                if (!((in >> (8 * j + 2 * t4 + i)) & 1)) s[nt][j][i] = -INFINITY;
         }
       }
-      if (PRE && more) load_k(row);
-      if (real) {
-        // running maximum and sum; p in bf16 terms: the scores' places are the A fragments' of the second product
-        uint32_t pf[NT][MT][AF][4];
+      __syncwarp();  // K's slot is free
+      if (more) {
+        in = __ballot_sync(0xffffffffu, row >= 0);
+        request(a.K, slot_at, row, in);
+      }
+      copies_commit();
+      // running maximum and sum; p in bf16 terms: the scores' places are the A fragments' of the second product
+      uint32_t pf[NT][MT][AF][4];
+      float corr[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float mx = -INFINITY, sum = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < 2 * MT; ++j) mx = fmaxf(mx, fmaxf(s[nt][j][0], s[nt][j][1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[nt], mx), mu = mn == -INFINITY ? 0.f : mn;
-          corr[nt] = exp2_ftz(m[nt] - mu);
-          m[nt] = mn;
+        for (int j = 0; j < 2 * MT; ++j) mx = fmaxf(mx, fmaxf(s[nt][j][0], s[nt][j][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[nt], mx), mu = mn == -INFINITY ? 0.f : mn;
+        corr[nt] = exp2_ftz(m[nt] - mu);
+        m[nt] = mn;
 #pragma unroll
-          for (int j = 0; j < 2 * MT; ++j) {
-            const float x = exp2_ftz(s[nt][j][0] - mu), y = exp2_ftz(s[nt][j][1] - mu);
-            sum += x + y;
-            uint32_t h, mm, ll;
-            split3(x, y, h, mm, ll);
-            uint32_t(&f)[AF][4] = pf[nt][j >> 1];
-            if constexpr (ONE) {
-              f[0][(j & 1) * 2] = g == 0 ? h : g == 1 ? ll : 0u;
-              f[0][(j & 1) * 2 + 1] = g == 0 ? mm : 0u;
-            } else {
-              f[0][(j & 1) * 2] = h;
-              f[0][(j & 1) * 2 + 1] = mm;
-              f[AF - 1][(j & 1) * 2] = 0u;
-              f[AF - 1][(j & 1) * 2 + 1] = ll;
-            }
+        for (int j = 0; j < 2 * MT; ++j) {
+          const float x = exp2_ftz(s[nt][j][0] - mu), y = exp2_ftz(s[nt][j][1] - mu);
+          sum += x + y;
+          uint32_t h, mm, ll;
+          split3(x, y, h, mm, ll);
+          uint32_t(&f)[AF][4] = pf[nt][j >> 1];
+          if constexpr (ONE) {
+            f[0][(j & 1) * 2] = g == 0 ? h : g == 1 ? ll : 0u;
+            f[0][(j & 1) * 2 + 1] = g == 0 ? mm : 0u;
+          } else {
+            f[0][(j & 1) * 2] = h;
+            f[0][(j & 1) * 2 + 1] = mm;
+            f[AF - 1][(j & 1) * 2] = 0u;
+            f[AF - 1][(j & 1) * 2 + 1] = ll;
           }
-          l[nt] = l[nt] * corr[nt] + sum;
         }
-        // o = o corr + p V
+        l[nt] = l[nt] * corr[nt] + sum;
+      }
+      copies_wait_all_but_one();  // this unit's V
+      // o = o corr + p V
+      const char* vp = mine + Shape::SLOT + 2 * t4 * PITCH + 16 * g;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if (!PRE) load_v(row, nb, nb + 1);
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int e0 = 0; e0 < 8; e0 += EN) {
+        for (int hv = 0; hv < (F32 ? 2 : 1); ++hv) {  // 16 bytes of V rows 2 t, + 1, + 8, + 9: eight channels, fp32 four
+          uint4 v[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[mt][i] = *reinterpret_cast<const uint4*>(vp + (16 * mt + (i & 1) + (i >> 1) * 8) * PITCH + 128 * (F32 ? 2 * nb + hv : nb));
+#pragma unroll
+          for (int e0 = 0; e0 < (F32 ? 4 : 8); e0 += EN) {
             float c[NT][EN][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              const Chunk<KT>* v = vc[nb] + 4 * mt;
               uint32_t b0[EN][SPL], b1[EN][SPL];
 #pragma unroll
               for (int i = 0; i < EN; ++i) {
                 const int e = e0 + i;
                 if constexpr (!F32) {
                   const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-                  b0[i][0] = __byte_perm(v[0].word(e >> 1), v[1].word(e >> 1), sel);
-                  b1[i][0] = __byte_perm(v[2].word(e >> 1), v[3].word(e >> 1), sel);
+                  b0[i][0] = __byte_perm(word_of(v[mt][0], e >> 1), word_of(v[mt][1], e >> 1), sel);
+                  b1[i][0] = __byte_perm(word_of(v[mt][2], e >> 1), word_of(v[mt][3], e >> 1), sel);
                 } else {
-                  split3(__uint_as_float(v[0].word(e)), __uint_as_float(v[1].word(e)), b0[i][0], b0[i][1], b0[i][2]);
-                  split3(__uint_as_float(v[2].word(e)), __uint_as_float(v[3].word(e)), b1[i][0], b1[i][1], b1[i][2]);
+                  split3(__uint_as_float(word_of(v[mt][0], e)), __uint_as_float(word_of(v[mt][1], e)), b0[i][0], b0[i][1], b0[i][2]);
+                  split3(__uint_as_float(word_of(v[mt][2], e)), __uint_as_float(word_of(v[mt][3], e)), b1[i][0], b1[i][1], b1[i][2]);
                 }
               }
 #pragma unroll
@@ -913,44 +908,41 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < EN; ++i) {
-                float(&d)[2] = o[nt][nb][e0 + i];
+                float(&d)[2] = o[nt][nb][4 * hv * (F32 ? 1 : 0) + e0 + i];
                 d[0] = fmaf(d[0], corr[nt], c[nt][i][0] + c[nt][i][2]);
                 d[1] = fmaf(d[1], corr[nt], c[nt][i][1] + c[nt][i][3]);
               }
           }
         }
       }
-      if (PRE && more) load_v(row, 0, NB);
-      const bool ends = real && cur.t + 1 == cur.nt;
-      if (real && (ends || !more)) {
-        __syncwarp();
-        put_part(started ? open_mine : part_mine);
-        __syncwarp();
+      __syncwarp();  // V's slot is free
+      if (more) request(a.V, slot_at + Shape::SLOT, row, in);
+      copies_commit();
+      const bool ends = cur.t + 1 == cur.nt;
+      if (ends || !more) {
+        finish();
         if (started && ends) {
-          const int j = cur.it / a.NQ, z = cur.it - j * a.NQ, gq = min(QR, a.G - z * QR);
-          const size_t out_row = ((size_t)cur.b * a.rows + j) * a.G + z * QR;
-#pragma unroll 1
-          for (int x = lane; x < gq * (DH / 4); x += 32) {
-            const int qn = x / (DH / 4), c = (x % (DH / 4)) * 4;
-            divide(out_row + qn, c, open_mine[QR * DH + qn], open_mine[QR * DH + QR + qn],
-                   *reinterpret_cast<const float4*>(open_mine + qn * DH + c));
+          output(cur);
+        } else if (!started) {
+          put_part(part_of(warp));
+        } else {
+          put_part(open_of(warp));
+          if (lane == 0) {
+            s_item[warp][0] = whi - 1 - cur.t;
+            s_item[warp][1] = whi - 1 - cur.t + cur.nt;
+            s_item[warp][2] = cur.b;
+            s_item[warp][3] = cur.it;
           }
-          __syncwarp();
-        } else if (started && lane == 0) {
-          s_item[warp][0] = whi - 1 - cur.t;
-          s_item[warp][1] = whi - 1 - cur.t + cur.nt;
-          s_item[warp][2] = cur.b;
-          s_item[warp][3] = cur.it;
         }
       }
       if (more) {
-        if (real) cur = nxt;
-        if (n + 2 < count) advance(nxt);
-        if (!PRE) row = pool_row(cur);
-        else if (n + 2 < count) row = pool_row(nxt);
+        cur = nxt;
+        if (n + 2 < count) {
+          advance(nxt);
+          row = pool_row(nxt);
+        }
         if (ends) started = true;
-        if (ends || n < 0) begin_item(cur);
-        if (n + 2 < count && nxt.t == 0) stage_q(nxt);
+        fresh = ends;
       }
     }
   }
@@ -968,12 +960,12 @@ __global__ void __launch_bounds__(PGA_THREADS, PagedShape<KT, NB, NTQ>::CTAS)
       int n, step;
       if (i < 9) {
         const int w = i & 7;
-        p0 = i < 8 ? reinterpret_cast<const float*>(s_q + w * Shape::QBYTES) : s_part;
-        p1 = s_part + (w + 1) * PARTF;
-        step = PARTF;
+        p0 = i < 8 ? open_of(w) : part_of(0);
+        p1 = part_of(w + 1);
+        step = Shape::WARP_BYTES / 4;
         n = 1;
-        while (w + n < PGA_WARPS && first_unit(w0 + w + n) < end) ++n;
-        if (i == 8 || end > first_unit(w0 + PGA_WARPS)) {
+        while (w + n < WARPS && first_unit(w0 + w + n) < end) ++n;
+        if (i == 8 || end > first_unit(w0 + WARPS)) {
           const int shared = i == 8 ? 9 : 10;
           dst = a.part + ((size_t)blockIdx.x * 2 + shared - 9) * PARTF;
           if (tid < 4) s_item[shared][tid] = it[tid];
