@@ -422,9 +422,9 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ unsigned sc[WARPS + 1];
   // items that cross warps or CTAs: first unit (-1: none), unit behind the last, row, item. 0..7: left open by that
-  // warp, which began it; 8: begun by an earlier CTA; 9 and 10: shared with earlier and with later CTAs
-  __shared__ int s_item[11][4];
-  __shared__ int s_last;
+  // warp, which began it; 8: begun by an earlier CTA
+  __shared__ int s_item[9][4];
+  __shared__ int s_last[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   int* s_pre = reinterpret_cast<int*>(smem_raw + WARPS * Shape::WARP_BYTES);  // [B + 1]
   // per warp: K rows, V rows (at the end of the stretch an item left open), what it adds to an item begun before it, q
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
   auto part_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES + 2 * Shape::SLOT); };
   auto open_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES); };
   griddep_launch();
-  if (tid < 11) s_item[tid][0] = -1;
+  if (tid < 9) s_item[tid][0] = -1;
   __syncthreads();
   griddep_wait();
 
@@ -445,11 +445,13 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
     if (hc != nh && blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_CLAMPED);
   }
   const int HR = a.rows * a.G;  // query rows of a request
-  int units = 0;
+  int units = 0, same = 0;  // units of all rows; of each where they are equal
   if (a.B <= 32) {  // every warp for itself, the same values: no barrier
     const int len = lane < a.B ? a.lens[lane] : 0;
     if (len > cap && blockIdx.x == 0 && warp == 0) raise_status(a.status, ST_CLAMPED);
     units = len > 0 ? (min(len, cap) + UNIT - 1) / UNIT : 0;
+    same = __shfl_sync(0xffffffffu, units, 0);
+    if (!__all_sync(0xffffffffu, lane >= a.B || units == same)) same = 0;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, units, x);
@@ -481,17 +483,34 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
   }
   const int IR = nh * a.NQ;     // items of a row
   const int U = units * IR;     // (below 2^31: checked on the host for the largest lengths)
-  const int CE = min((int)gridDim.x, (U + WARPS - 1) / WARPS);  // CTAs with work
+  // CTA c takes the units from cta_first(c) on, its warps equal stretches of them. Rows of one length: each CTA has whole
+  // items, or each item has whole CTAs, where that takes (nearly) as few units a warp; else CTAs share evenly.
+  int CE = min((int)gridDim.x, (U + WARPS - 1) / WARPS);  // CTAs with work
+  int group = U, ctas = CE;                               // `ctas` CTAs share each `group` units
+  if (same > 0) {
+    const int items = a.B * IR;
+    if (same <= WARPS) {
+      const int per = WARPS / same, need = (items + per - 1) / per;
+      if (need <= (int)gridDim.x) group = per * same, ctas = 1, CE = need;
+    } else {
+      const int per = min((int)gridDim.x / max(items, 1), (same + WARPS - 1) / WARPS);
+      const int even = (U + WARPS * CE - 1) / (WARPS * CE);
+      if (per > 0 && (same + WARPS * per - 1) / (WARPS * per) * 16 <= even * 17) group = same, ctas = per, CE = items * per;
+    }
+  }
   if ((int)blockIdx.x >= CE) return;
-  // Warp w's stretch is [first(w), first(w + 1)): U / NW units, one more for the first U % NW
-  const int NW = CE * WARPS, w0 = blockIdx.x * WARPS;
-  const int each = U / NW, extra = U - each * NW;
-  auto first_unit = [&](int w) { return w * each + min(w, extra); };
-  auto cta_of = [&](int u) {
-    const int big = extra * (each + 1);
-    return (u < big ? u / (each + 1) : extra + (u - big) / each) / WARPS;  // (u >= big only if each > 0)
+  const int each = group / ctas, extra = group - each * ctas;
+  auto cta_first = [&](int c) {
+    const int gr = c / ctas, p = c - gr * ctas;
+    return min(U, gr * group + p * each + min(p, extra));
   };
-  const int wlo = first_unit(w0 + warp), whi = first_unit(w0 + warp + 1);
+  auto cta_of = [&](int u) {
+    const int gr = u / group, r = u - gr * group, big = extra * (each + 1);
+    return gr * ctas + (r < big ? r / (each + 1) : extra + (r - big) / each);  // (r >= big only if each > 0)
+  };
+  const int clo = cta_first(blockIdx.x), chi = cta_first(blockIdx.x + 1);
+  auto warp_first = [&](int w) { return clo + w * ((chi - clo) / WARPS) + min(w, (chi - clo) % WARPS); };
+  const int wlo = warp_first(warp), whi = warp_first(warp + 1);
   const int row_bytes = a.dh * (int)sizeof(KT);
 
   auto locate = [&](int u) {
@@ -669,14 +688,14 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
       if (a.lse && t4 == 0) a.lse[row] = log_sum(m[nt], l[nt]);
     }
   };
-  // n partials, the first at p0 and the others from p1 on, `step` floats apart, added in that order by all warps: into
-  // a partial `dst`, or divided into the outputs of item (b, it). Eight at a time, so that their loads overlap.
+  // n partials, the first at p0 and the others from p1 on, `step` floats apart, added in that order by all warps (one
+  // query: by this warp): into a partial `dst`, or divided into the outputs of item (b, it). Eight at a time, so that their loads overlap.
   auto combine = [&](const float* p0, const float* p1, int step, int n, int b, int it, float* dst) {
     const int j = it / a.NQ, z = it - j * a.NQ;
     const int gq = min(QR, a.G - z * QR);
     const size_t row = ((size_t)b * a.rows + j) * a.G + z * QR;
 #pragma unroll 1
-    for (int x = tid; x < gq * (DH / 4); x += THREADS) {
+    for (int x = ONE ? lane : tid; x < gq * (DH / 4); x += ONE ? 32 : THREADS) {
       const int qn = x / (DH / 4), c = (x % (DH / 4)) * 4;
       float top = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -948,50 +967,46 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
   }
   __syncthreads();
 
-  // What crosses warps or CTAs, item by item: those of this CTA (0..8), then those shared with other CTAs, by the last
-  // CTA to arrive. Partials are added in the order of their warps, then of their CTAs.
+  // What crosses warps: item by item, its partials in the order of their warps; by all warps, items of one query by a
+  // warp each. What crosses CTAs too goes to the workspace, and the last CTA to arrive adds the CTAs' partials in order.
+  auto sync = [&]() {
+    if constexpr (ONE) __syncwarp();
+    else __syncthreads();
+  };
+  const bool first = ONE ? lane == 0 : tid == 0;
 #pragma unroll 1
-  for (int i = 0; i < 11; ++i) {
-    int* it = s_item[i];
-    const int begin = it[0], end = it[1];
-    if (begin >= 0) {
-      const float *p0, *p1;
-      float* dst = nullptr;
-      int n, step;
-      if (i < 9) {
-        const int w = i & 7;
-        p0 = i < 8 ? open_of(w) : part_of(0);
-        p1 = part_of(w + 1);
-        step = Shape::WARP_BYTES / 4;
-        n = 1;
-        while (w + n < WARPS && first_unit(w0 + w + n) < end) ++n;
-        if (i == 8 || end > first_unit(w0 + WARPS)) {
-          const int shared = i == 8 ? 9 : 10;
-          dst = a.part + ((size_t)blockIdx.x * 2 + shared - 9) * PARTF;
-          if (tid < 4) s_item[shared][tid] = it[tid];
-        }
-      } else {
-        const int c0 = cta_of(begin);
-        n = cta_of(end - 1) - c0 + 1;
-        __syncthreads();
-        if (tid == 0) {
-          const unsigned old = atomicAdd(a.tick + c0, 1u);
-          s_last = old == (unsigned)(n - 1);
-          if (s_last) a.tick[c0] = 0;
-          __threadfence();
-        }
-        __syncthreads();
-        p0 = a.part + ((size_t)c0 * 2 + 1) * PARTF;  // begun in c0, carried on in the next CTAs
-        p1 = a.part + ((size_t)c0 + 1) * 2 * PARTF;
-        step = 2 * PARTF;
-        if (!s_last) n = 0;
-      }
-      if (n > 0) combine(p0, p1, step, n, it[2], it[3], dst);
-    }
-    if (i == 8) {
+  for (int i = ONE ? warp : 0; i < 9; i += ONE ? WARPS : 1) {
+    const int begin = s_item[i][0], end = s_item[i][1], b = s_item[i][2], it = s_item[i][3];
+    if (begin < 0) continue;
+    const int w = i & 7;  // (item 8 starts with warp 0)
+    const float *p0 = i < 8 ? open_of(w) : part_of(0), *p1 = part_of(w + 1);
+    int n = 1, step = Shape::WARP_BYTES / 4;
+    while (w + n < WARPS && warp_first(w + n) < min(end, chi)) ++n;
+    const bool shared = i == 8 || end > chi;
+    float* dst = shared ? a.part + ((size_t)blockIdx.x * 2 + (i == 8 ? 0 : 1)) * PARTF : nullptr;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      combine(p0, p1, step, n, b, it, dst);
+      if (!dst) break;
+      const int c0 = cta_of(begin);
+      n = cta_of(end - 1) - c0 + 1;
       __threadfence();
-      __syncthreads();
-      if (s_item[9][0] < 0 && s_item[10][0] < 0) return;
+      sync();
+      int last = 0;
+      if (first) {
+        last = atomicAdd(a.tick + c0, 1u) == (unsigned)(n - 1);
+        if (last) a.tick[c0] = 0;
+        __threadfence();
+        s_last[ONE ? warp : 0] = last;
+      }
+      sync();
+      last = s_last[ONE ? warp : 0];
+      sync();
+      if (!last) break;
+      p0 = a.part + ((size_t)c0 * 2 + 1) * PARTF;  // begun in c0, carried on in the next CTAs
+      p1 = a.part + ((size_t)c0 + 1) * 2 * PARTF;
+      step = 2 * PARTF;
+      dst = nullptr;
     }
   }
 }
