@@ -465,47 +465,55 @@ class PagedKV:
                 raise ValueError(f"{n} must be a CUDA tensor")
         if n_pages > 1 and K.stride(0) != V.stride(0):
             raise ValueError(f"K and V pages lie at different distances: {K.stride(0)} and {V.stride(0)}")
-        self.K, self.V, self.device = K, V, K.device
+        self.K, self.V, self.index = K, V, K.get_device()
         self.n_pages, self.h_kv, self.page, self.dh = n_pages, h_kv, page, dh
         self.c = PagedKVC(_wdt(K), K.data_ptr(), V.data_ptr(), K.stride(0) if n_pages > 1 else 0, n_pages, page, h_kv, dh)
         self.ref = ctypes.byref(self.c)
 
 
-def _arg(t: Optional[torch.Tensor], dtype, shape, device, name: str) -> Optional[int]:
-    """Pointer of a contiguous tensor of this dtype, shape and device (None stays None)."""
+def _arg(t: Optional[torch.Tensor], dtype, shape, index: int, name: str) -> Optional[int]:
+    """Pointer of a contiguous tensor of this dtype and shape on CUDA device `index` (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}; expected {shape} "
-                         f"{dtype} on {device}, contiguous")
+                         f"{dtype} on cuda:{index}, contiguous")
     return t.data_ptr()
 
 
-def _ws_arg(ws: torch.Tensor, device) -> int:
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws: {ws.dtype} on {ws.device}; expected a workspace on {device}")
+def _ws_arg(ws: torch.Tensor, index: int) -> int:
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws: {ws.dtype} on {ws.device}; expected a workspace on cuda:{index}")
     return ws.data_ptr()
 
 
-def _launch(fn, name: str, device, stream, *args):
-    """fn(*args, stream) on the tensors' own device: its current stream unless one is given."""
-    if not device.type == "cuda":
-        raise ValueError(f"{name}: CUDA tensors are needed, got {device}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{name}: a stream of {stream.device} for tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        s = fn(*args, _stream(stream))
+_i32, _f32 = torch.int32, torch.float32
+
+
+def _launch(fn, name: str, index: int, stream, *args):
+    """fn(*args, stream) on CUDA device `index`, the tensors' own: its current stream unless one is given."""
+    if index < 0:
+        raise ValueError(f"{name}: CUDA tensors are needed")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index == index:
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            s = fn(*args, _stream(stream))
-    _check(s, name)
+        raise ValueError(f"{name}: a stream of {stream.device} for tensors on cuda:{index}")
+    if torch._C._cuda_getDevice() == index:
+        s = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            s = fn(*args, raw)
+    if s != DV_OK:
+        raise DvError(s, name)
 
 
 def dv_page_tables(want, lens, lens_out, table, free_list, free_count, free_count_out, slots, offsets, granted, page, ws,
                    stream=None):
     """Block tables [R][W], slots and the free stack from the requests'
     current and wanted lengths (int32, on the device)."""
-    dev, i32 = want.device, torch.int32
+    dev, i32 = want.get_device(), _i32
     R, W = table.shape
     n_pages, max_tokens = free_list.shape[0], slots.shape[0]
     _launch(_lib_dv_page_tables, "dv_page_tables", dev, stream, _arg(want, i32, (R,), dev, "want"), R, int(page), n_pages, W,
@@ -518,12 +526,12 @@ def dv_page_tables(want, lens, lens_out, table, free_list, free_count, free_coun
 
 def dv_paged_append(kv: PagedKV, k, v, slots, ws, stream=None):
     """k, v [T][h_kv][dh] fp32 of new tokens into their slots [T] of the pools."""
-    dev, T = kv.device, slots.shape[0]
+    dev, T = kv.index, slots.shape[0]
     shape = (T, kv.h_kv, kv.dh)
     if T == 0:
         return
-    _launch(_lib_dv_paged_append, "dv_paged_append", dev, stream, kv.ref, _arg(k, torch.float32, shape, dev, "k"),
-            _arg(v, torch.float32, shape, dev, "v"), T, _arg(slots, torch.int32, (T,), dev, "slots"), _ws_arg(ws, dev),
+    _launch(_lib_dv_paged_append, "dv_paged_append", dev, stream, kv.ref, _arg(k, _f32, shape, dev, "k"),
+            _arg(v, _f32, shape, dev, "v"), T, _arg(slots, _i32, (T,), dev, "slots"), _ws_arg(ws, dev),
             ws.numel())
 
 
@@ -532,7 +540,7 @@ def dv_paged_attn(q, kv: PagedKV, table, lens, scale, out, ws, lse=None, head_id
     [B][h_q][dh]; with a set head_idx / head_count of key-value heads they are
     [B][kh_max * G][dh], G query heads for each place of the set, kh_max =
     len(head_idx), and h_q = G * h_kv."""
-    dev, i32, f32 = kv.device, torch.int32, torch.float32
+    dev, i32, f32 = kv.index, _i32, _f32
     B, rows, dh = q.shape
     heads = kv.h_kv if head_idx is None else head_idx.shape[0]
     if head_idx is not None and head_count is None or heads == 0 or rows % heads != 0 or dh != kv.dh:
@@ -548,7 +556,7 @@ def dv_paged_attn(q, kv: PagedKV, table, lens, scale, out, ws, lse=None, head_id
 def dv_sparse_mha_paged(y, Wqkv, bqkv, WOt, bO, kv: PagedKV, table, lens, slots, scale, head_idx, head_count, kh_max, out,
                         ws, accumulate=False, exact_kv=False, stream=None):
     """dv_sparse_mha over a paged cache: per-row lengths [B], the new token's slot [B]."""
-    dev, i32, f32 = kv.device, torch.int32, torch.float32
+    dev, i32, f32 = kv.index, _i32, _f32
     B, d = y.shape
     h, dh, W = kv.h_kv, kv.dh, table.shape[1]
     if head_idx.shape[0] < kh_max:
