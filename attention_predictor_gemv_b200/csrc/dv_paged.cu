@@ -13,28 +13,28 @@ constexpr int CTAS_PER_SM = 2;  // of the attention kernel, at most
 bool dtype_ok(int t) { return t == DV_F32 || t == DV_BF16; }
 int blocks64(int dh) { return dh <= 64 ? 1 : dh <= 128 ? 2 : 4; }
 
-template <typename KT, int NB, int NT>
+template <typename KT, int NB, int QR>
 cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
-  using Shape = PagedShape<KT, NB, NT>;
+  using Shape = PagedShape<KT, NB, QR>;
   constexpr int per_sm = Shape::CTAS, UNIT = Shape::UNIT;
-  static_assert(per_sm <= CTAS_PER_SM && Shape::PARTF <= 16 * (Shape::DH + 2), "partial slots");
+  static_assert((per_sm == 1 || (NB == 1 && per_sm == CTAS_PER_SM)) && Shape::PARTF <= 16 * (Shape::DH + 2), "partial slots");
   a.NQ = (a.G + Shape::QR - 1) / Shape::QR;
   const size_t smem = (size_t)Shape::WARPS * Shape::WARP_BYTES + 4ull * (a.B + 1);
-  cudaError_t e = allow_smem(paged_attn_kernel<KT, NB, NT>, smem);
+  cudaError_t e = allow_smem(paged_attn_kernel<KT, NB, QR>, smem);
   if (e != cudaSuccess) return e;
   const long long cap = (long long)a.W * a.page;
   const long long most = a.B * ((cap + UNIT - 1) / UNIT) * (long long)a.rows * a.NQ;  // units, at most
   const long long want = (most + Shape::WARPS - 1) / Shape::WARPS, have = (long long)sm_count() * per_sm;
-  return launch_main(paged_attn_kernel<KT, NB, NT>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
+  return launch_main(paged_attn_kernel<KT, NB, QR>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
                      dim3(32 * Shape::WARPS), smem, st, a);
 }
 
 template <typename KT>
 cudaError_t launch_attn_kt(const PagedAttnArgs& a, cudaStream_t st) {
   switch (blocks64(a.dh)) {
-    case 1: return a.G == 1 ? launch_attn<KT, 1, 0>(a, st) : a.G > 8 ? launch_attn<KT, 1, 2>(a, st) : launch_attn<KT, 1, 1>(a, st);
-    case 2: return a.G == 1 ? launch_attn<KT, 2, 0>(a, st) : a.G > 8 ? launch_attn<KT, 2, 2>(a, st) : launch_attn<KT, 2, 1>(a, st);
-    default: return a.G == 1 ? launch_attn<KT, 4, 0>(a, st) : launch_attn<KT, 4, 1>(a, st);
+    case 1: return a.G == 1 ? launch_attn<KT, 1, 1>(a, st) : a.G > 8 ? launch_attn<KT, 1, 16>(a, st) : launch_attn<KT, 1, 8>(a, st);
+    case 2: return a.G == 1 ? launch_attn<KT, 2, 1>(a, st) : a.G > 8 ? launch_attn<KT, 2, 16>(a, st) : launch_attn<KT, 2, 8>(a, st);
+    default: return a.G == 1 ? launch_attn<KT, 4, 1>(a, st) : launch_attn<KT, 4, 8>(a, st);
   }
 }
 
@@ -45,7 +45,8 @@ long long stride_rows(const dv_paged_kv* kv) {
 }  // namespace
 
 size_t paged_attn_part_floats(int dh) {
-  return (size_t)CTAS_PER_SM * sm_count() * 2 * 16 * (64 * blocks64(dh) + 2);
+  // two slots per CTA and as many for groups of CTAs; only 64 channels or fewer run two CTAs on an SM
+  return (size_t)(dh <= 64 ? CTAS_PER_SM : 1) * sm_count() * 4 * 16 * (64 * blocks64(dh) + 2);
 }
 
 dv_status paged_kv_check(const dv_paged_kv* kv) {

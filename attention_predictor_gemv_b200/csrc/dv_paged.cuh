@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_token_kernel(PagedTokenArgs 
 // staging and no barrier in the loop; the next unit's K is requested once the
 // scores of this one are formed, its V once this one's is used.
 // ----------------------------------------------------------------------------
-constexpr int PGA_MAX_WARPS = 8;
+constexpr int PGA_JOIN = 16;  // CTAs' partials that one CTA adds, at most (of more, groups first)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -383,23 +383,24 @@ struct PagedAt {
   int b, it, t, nt, len;
 };
 
-// Shape of a kernel for NB blocks of 64 channels and NT groups of 8 query heads
-// (NT = 0: one query head, its bf16 terms in three rows of one group): warps of
-// a CTA, 16-key tiles in a unit, CTAs per SM, query rows, floats of a partial
-// ([QR][DH] sums, then QR maxima and QR weight sums), and shared memory per
-// warp: K and V rows of a unit, a partial, the next item's q.
-template <typename KT, int NB, int NT>
+// Shape of a kernel for NB blocks of 64 channels and up to QR query heads of a
+// key-value head: 1 (its bf16 terms in three rows of the 16), 8 (high terms
+// above middle ones) or 16 (each term a fragment of its own): warps of a CTA,
+// 16-key tiles in a unit, CTAs per SM, floats of a partial ([QR][DH] sums, then
+// QR maxima and QR weight sums), and shared memory per warp: K and V rows of a
+// unit, a partial, the next item's q.
+template <typename KT, int NB, int QR_>
 struct PagedShape {
   static constexpr int DH = 64 * NB;
   static constexpr int ROW = DH * sizeof(KT);  // bytes
   static constexpr int PITCH = ROW + 16;       // of rows in shared memory: 16-byte pieces of neighbours in other banks
   static constexpr int WARPS = ROW <= 512 ? 8 : 4;
-  static constexpr int MT = ROW <= 256 && NT <= 1 ? 2 : 1;
+  static constexpr int QR = QR_;
+  static constexpr int MT = ROW <= 128 || (ROW <= 256 && QR <= 8) ? 2 : 1;
   static constexpr int UNIT = 16 * MT;
-  static constexpr int CTAS = ROW == 128 && NT <= 1 ? 2 : 1;
-  static constexpr int QR = NT == 0 ? 1 : 8 * NT;
+  static constexpr int CTAS = ROW == 128 && QR <= 8 ? 2 : 1;
   static constexpr int PARTF = (QR * (DH + 2) + 3) & ~3;
-  static constexpr bool STAGE = NT == 0 || (NT == 1 && NB <= 2);  // the next item's q is copied ahead
+  static constexpr bool STAGE = QR == 1 || (QR == 8 && NB <= 2);  // the next item's q is copied ahead
   static constexpr int RAWF = STAGE ? QR * DH : 0;
   static constexpr int SLOT = UNIT * PITCH;
   static constexpr int WARP_BYTES = 2 * SLOT + 4 * (PARTF + RAWF);
@@ -407,18 +408,18 @@ struct PagedShape {
   static_assert(WARPS * WARP_BYTES + 4 * (PAGED_MAX_ROWS + 1) + 1024 <= 227 * 1024, "shared memory");
 };
 
-template <typename KT, int NB, int NTQ>
-__global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShape<KT, NB, NTQ>::CTAS)
+template <typename KT, int NB, int QR>
+__global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape<KT, NB, QR>::CTAS)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
-  using Shape = PagedShape<KT, NB, NTQ>;
-  constexpr bool F32 = sizeof(KT) == 4, ONE = NTQ == 0;
-  constexpr int NT = ONE ? 1 : NTQ;
-  constexpr int MT = Shape::MT, UNIT = Shape::UNIT, DH = Shape::DH, QR = Shape::QR, PARTF = Shape::PARTF;
+  using Shape = PagedShape<KT, NB, QR>;
+  constexpr bool F32 = sizeof(KT) == 4, ONE = QR == 1, WIDE = QR == 16;
+  constexpr int MT = Shape::MT, UNIT = Shape::UNIT, DH = Shape::DH, PARTF = Shape::PARTF;
   constexpr int WARPS = Shape::WARPS, THREADS = 32 * WARPS, ROW = Shape::ROW, PITCH = Shape::PITCH;
   constexpr int SPL = F32 ? 3 : 1;  // bf16 terms of a cache element
-  constexpr int AF = ONE ? 1 : 2;   // A fragments that hold the terms of q, and of p
+  constexpr int AF = ONE ? 1 : WIDE ? 3 : 2;  // A fragments that hold the terms of q, and of p
+  constexpr int QH = WIDE ? 2 : 1;  // query rows of a lane: g, and g + 8
   constexpr int NK = 4 * NB;        // MMA steps over the channels
-  constexpr int EN = F32 || NT > 1 ? 2 : 4;  // channel tiles whose products run side by side
+  constexpr int EN = F32 ? 2 : 4;  // channel tiles whose products run side by side
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ unsigned sc[WARPS + 1];
   // items that cross warps or CTAs: first unit (-1: none), unit behind the last, row, item. 0..7: left open by that
@@ -578,8 +579,9 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
     }
   };
 
-  float o[NT][NB][8][2], m[NT], l[NT];  // query row g; l: this lane's keys
-  uint32_t qa[NT][NK][4], ql[ONE ? 1 : NT][NK][2];
+  float o[NB][8][QH][2], m[QH], l[QH];  // (l: this lane's keys)
+  uint32_t qa[NK][4], ql[ONE ? 1 : NK][2], qw[WIDE ? NK : 1][4];  // (WIDE: high, -, middle; low in ql and qx)
+  uint32_t qx[WIDE ? NK : 1][2];
   float* raw_mine = part_of(warp) + PARTF;
   // q of an item on its way to shared memory
   auto stage_q = [&](const PagedAt& p) {
@@ -593,86 +595,94 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
     }
   };
   // q of an item as A fragments: rows 0-7 its high terms, rows 8-15 the middle ones, and the low ones in rows 8-15 of
-  // another; of one query row 0 is high, row 8 middle, row 1 low. An MMA step takes from lane t four channels that K's
+  // another; of one query row 0 is high, row 8 middle, row 1 low; of 16 queries each term has its fragment. An MMA step takes from lane t four channels that K's
   // fragments have there: half of the 16 bytes (bf16) or the 16 bytes (fp32) that it reads, pieces 2 t and 2 t + 1 of
   // every 128 bytes of the row.
   auto begin_item = [&](const PagedAt& p) {
     const int j = p.it / a.NQ, z = p.it - j * a.NQ;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = ONE ? 0 : (z * NT + nt) * 8 + g;
-      const float* qr = Shape::STAGE ? raw_mine + (ONE ? 0 : g) * DH : a.q + (((size_t)p.b * a.rows + j) * a.G + n) * a.dh;
+    for (int h = 0; h < QH; ++h) {
+      const int r = ONE ? 0 : g + 8 * h, n = z * QR + r;
+      const float* qr = Shape::STAGE ? raw_mine + r * DH : a.q + (((size_t)p.b * a.rows + j) * a.G + n) * a.dh;
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
         const int c = F32 ? 32 * (s >> 1) + 8 * t4 + 4 * (s & 1) : 64 * (s >> 2) + 16 * t4 + 4 * (s & 3);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (n < a.G && c < a.dh) x = *reinterpret_cast<const float4*>(qr + c);
-        uint2 h, mm, ll;
-        split3(x.x, x.y, h.x, mm.x, ll.x);
-        split3(x.z, x.w, h.y, mm.y, ll.y);
+        uint2 hi, mm, ll;
+        split3(x.x, x.y, hi.x, mm.x, ll.x);
+        split3(x.z, x.w, hi.y, mm.y, ll.y);
         if constexpr (ONE) {
-          qa[nt][s][0] = g == 0 ? h.x : g == 1 ? ll.x : 0u;
-          qa[nt][s][1] = g == 0 ? mm.x : 0u;
-          qa[nt][s][2] = g == 0 ? h.y : g == 1 ? ll.y : 0u;
-          qa[nt][s][3] = g == 0 ? mm.y : 0u;
+          qa[s][0] = g == 0 ? hi.x : g == 1 ? ll.x : 0u;
+          qa[s][1] = g == 0 ? mm.x : 0u;
+          qa[s][2] = g == 0 ? hi.y : g == 1 ? ll.y : 0u;
+          qa[s][3] = g == 0 ? mm.y : 0u;
+        } else if constexpr (WIDE) {
+          qa[s][h] = hi.x;
+          qa[s][2 + h] = hi.y;
+          qw[s][h] = mm.x;
+          qw[s][2 + h] = mm.y;
+          (h ? qx : ql)[s][0] = ll.x;
+          (h ? qx : ql)[s][1] = ll.y;
         } else {
-          qa[nt][s][0] = h.x;
-          qa[nt][s][1] = mm.x;
-          qa[nt][s][2] = h.y;
-          qa[nt][s][3] = mm.y;
-          ql[nt][s][0] = ll.x;
-          ql[nt][s][1] = ll.y;
+          qa[s][0] = hi.x;
+          qa[s][1] = mm.x;
+          qa[s][2] = hi.y;
+          qa[s][3] = mm.y;
+          ql[s][0] = ll.x;
+          ql[s][1] = ll.y;
         }
       }
-      m[nt] = -INFINITY;
-      l[nt] = 0.f;
+      m[h] = -INFINITY;
+      l[h] = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[nt][nb][e][0] = o[nt][nb][e][1] = 0.f;
+        for (int e = 0; e < 8; ++e) o[nb][e][h][0] = o[nb][e][h][1] = 0.f;
     }
     __syncwarp();
   };
   // The warp's sums complete: l over the lanes of a query, one query's low terms (row 1) added to row 0
   auto finish = [&]() {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
-      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
-      if constexpr (ONE) {
+    for (int h = 0; h < QH; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    if constexpr (ONE) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) o[nt][nb][e][i] += __shfl_xor_sync(0xffffffffu, o[nt][nb][e][i], 4);
-      }
+          for (int i = 0; i < 2; ++i) o[nb][e][0][i] += __shfl_xor_sync(0xffffffffu, o[nb][e][0][i], 4);
     }
   };
-  // Row g of group nt times f, `dh` channels, to d. Tile e of block nb holds channels 64 nb + 8 (2 t + i) + e (bf16) or
+  // A lane's row h times f, `dh` channels, to d. Tile e of block nb holds channels 64 nb + 8 (2 t + i) + e (bf16) or
   // 64 nb + 32 (e / 4) + 4 (2 t + i) + e % 4 (fp32: a lane's 16 bytes of a V row are four channels).
-  auto store_row = [&](int nt, float* d, int dh, float f) {
+  auto store_row = [&](int h, float* d, int dh, float f) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = 64 * nb + (F32 ? 32 * h + 8 * t4 + 4 * i : 16 * t4 + 8 * i + 4 * h);
-          const float(*v)[2] = o[nt][nb] + 4 * h;
-          if (c < dh) *reinterpret_cast<float4*>(d + c) = make_float4(v[0][i] * f, v[1][i] * f, v[2][i] * f, v[3][i] * f);
+        for (int e = 0; e < 8; e += 4) {
+          const int c = 64 * nb + (F32 ? 8 * e + 8 * t4 + 4 * i : 16 * t4 + 8 * i + e);
+          if (c < dh)
+            *reinterpret_cast<float4*>(d + c) =
+                make_float4(o[nb][e][h][i] * f, o[nb][e + 1][h][i] * f, o[nb][e + 2][h][i] * f, o[nb][e + 3][h][i] * f);
         }
   };
   auto put_part = [&](float* d) {
     if (ONE && g > 0) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = ONE ? 0 : nt * 8 + g;
+    for (int h = 0; h < QH; ++h) {
+      const int n = ONE ? 0 : g + 8 * h;
       if (t4 == 0) {
-        d[QR * DH + n] = m[nt];
-        d[QR * DH + QR + n] = l[nt];
+        d[QR * DH + n] = m[h];
+        d[QR * DH + QR + n] = l[h];
       }
-      store_row(nt, d + n * DH, DH, 1.f);
+      store_row(h, d + n * DH, DH, 1.f);
     }
   };
   const auto inverse = [](float sum) { return sum > 0.f || sum != sum ? 1.f / sum : 0.f; };  // (NaN stays)
@@ -680,12 +690,12 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
   auto output = [&](const PagedAt& p) {
     const int j = p.it / a.NQ, z = p.it - j * a.NQ;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = z * QR + (ONE ? 0 : nt * 8 + g);
+    for (int h = 0; h < QH; ++h) {
+      const int n = z * QR + (ONE ? 0 : g + 8 * h);
       if (ONE ? g > 0 : n >= a.G) continue;
       const size_t row = ((size_t)p.b * a.rows + j) * a.G + n;
-      store_row(nt, a.out + row * a.dh, a.dh, inverse(l[nt]));
-      if (a.lse && t4 == 0) a.lse[row] = log_sum(m[nt], l[nt]);
+      store_row(h, a.out + row * a.dh, a.dh, inverse(l[h]));
+      if (a.lse && t4 == 0) a.lse[row] = log_sum(m[h], l[h]);
     }
   };
   // n partials, the first at p0 and the others from p1 on, `step` floats apart, added in that order by all warps (one
@@ -778,9 +788,11 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
       if (fresh) begin_item(cur);
       if (more && nxt.t == 0) stage_q(nxt);  // (lands with the next unit's K)
       // scores of UNIT keys by QR queries
-      float s[NT][2 * MT][2];  // scores, then weights, of keys 8 j + 2 t and + 1
+      float s[QH][2 * MT][2];  // scores, then weights, of keys 8 j + 2 t and + 1
       {
-        float c[NT][2 * MT][4];
+        // two sums where few would leave the tensor cores waiting for one another
+        constexpr int CN = !ONE && MT == 1 ? 2 : 1;
+        float c[CN][2 * MT][4];
 #pragma unroll
         for (int k = 0; k < NK; k += F32 ? 1 : 2) {
           // 16 bytes of a K row: eight channels (two steps), fp32 four (one)
@@ -800,42 +812,58 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
             }
           }
 #pragma unroll
-          for (int h = 0; h < (F32 ? 1 : 2); ++h)
+          for (int h = 0; h < (F32 ? 1 : 2); ++h) {
+            // products from the smallest on, those of one score apart
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              // products from the smallest on, those of one score apart
+            for (int t = SPL - 1; t >= 0; --t) {
 #pragma unroll
-              for (int t = SPL - 1; t >= 0; --t)
+              for (int j = 0; j < 2 * MT; ++j) {
+                if (k + h == 0 && t == SPL - 1) mma_bf16_first(c[0][j], qa[k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
+                else mma_bf16(c[0][j], qa[k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
+              }
+              if constexpr (WIDE) {
+                if (t < 2) {
 #pragma unroll
-                for (int j = 0; j < 2 * MT; ++j) {
-                  if (k + h == 0 && t == SPL - 1) mma_bf16_first(c[nt][j], qa[nt][k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
-                  else mma_bf16(c[nt][j], qa[nt][k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
+                  for (int j = 0; j < 2 * MT; ++j) {
+                    if (CN > 1 && k + h == 0 && t == (SPL > 1 ? 1 : 0)) mma_bf16_first(c[CN - 1][j], qw[k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
+                    else mma_bf16(c[CN - 1][j], qw[k + h], b0[j][F32 ? t : h], b1[j][F32 ? t : h]);
+                  }
                 }
-              if constexpr (!ONE) {
-                const uint32_t low[4] = {0u, ql[nt][k + h][0], 0u, ql[nt][k + h][1]};
-#pragma unroll
-                for (int j = 0; j < 2 * MT; ++j) mma_bf16(c[nt][j], low, b0[j][F32 ? 0 : h], b1[j][F32 ? 0 : h]);
               }
             }
+            if constexpr (!ONE) {
+              const uint32_t low[4] = {WIDE ? ql[k + h][0] : 0u, WIDE ? qx[WIDE ? k + h : 0][0] : ql[k + h][0],
+                                       WIDE ? ql[k + h][1] : 0u, WIDE ? qx[WIDE ? k + h : 0][1] : ql[k + h][1]};
+#pragma unroll
+              for (int j = 0; j < 2 * MT; ++j) {
+                if (CN > 1 && !WIDE && k + h == 0) mma_bf16_first(c[CN - 1][j], low, b0[j][F32 ? 0 : h], b1[j][F32 ? 0 : h]);
+                else mma_bf16(c[CN - 1][j], low, b0[j][F32 ? 0 : h], b1[j][F32 ? 0 : h]);
+              }
+            }
+          }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < 2 * MT; ++j)
 #pragma unroll
-          for (int j = 0; j < 2 * MT; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float v = c[nt][j][i] + c[nt][j][2 + i];
-              if constexpr (ONE) v += __shfl_xor_sync(0xffffffffu, v, 4);  // row 1's: rows 0 and 1 get the score
-              s[nt][j][i] = v * a.scale_log2;
+          for (int i = 0; i < 2; ++i) {
+            float v[2] = {c[0][j][i], c[0][j][2 + i]};
+            if constexpr (CN > 1) {
+              v[0] += c[1][j][i];
+              v[1] += c[1][j][2 + i];
             }
+            if constexpr (!WIDE) v[0] += v[1];
+            if constexpr (ONE) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);  // row 1's: rows 0 and 1 get the score
+#pragma unroll
+            for (int h = 0; h < QH; ++h) s[h][j][i] = v[h] * a.scale_log2;
+          }
         if (in != ~0u) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int h = 0; h < QH; ++h)
 #pragma unroll
             for (int j = 0; j < 2 * MT; ++j)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (!((in >> (8 * j + 2 * t4 + i)) & 1)) s[nt][j][i] = -INFINITY;
+                if (!((in >> (8 * j + 2 * t4 + i)) & 1)) s[h][j][i] = -INFINITY;
         }
       }
       __syncwarp();  // K's slot is free
@@ -845,36 +873,41 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
       }
       copies_commit();
       // running maximum and sum; p in bf16 terms: the scores' places are the A fragments' of the second product
-      uint32_t pf[NT][MT][AF][4];
-      float corr[NT];
+      uint32_t pf[MT][AF][4];
+      float corr[QH];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int h = 0; h < QH; ++h) {
         float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) mx = fmaxf(mx, fmaxf(s[nt][j][0], s[nt][j][1]));
+        for (int j = 0; j < 2 * MT; ++j) mx = fmaxf(mx, fmaxf(s[h][j][0], s[h][j][1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[nt], mx), mu = mn == -INFINITY ? 0.f : mn;
-        corr[nt] = exp2_ftz(m[nt] - mu);
-        m[nt] = mn;
+        const float mn = fmaxf(m[h], mx), mu = mn == -INFINITY ? 0.f : mn;
+        corr[h] = exp2_ftz(m[h] - mu);
+        m[h] = mn;
 #pragma unroll
         for (int j = 0; j < 2 * MT; ++j) {
-          const float x = exp2_ftz(s[nt][j][0] - mu), y = exp2_ftz(s[nt][j][1] - mu);
+          const float x = exp2_ftz(s[h][j][0] - mu), y = exp2_ftz(s[h][j][1] - mu);
           sum += x + y;
-          uint32_t h, mm, ll;
-          split3(x, y, h, mm, ll);
-          uint32_t(&f)[AF][4] = pf[nt][j >> 1];
+          uint32_t hi, mm, ll;
+          split3(x, y, hi, mm, ll);
+          uint32_t(&f)[AF][4] = pf[j >> 1];
+          const int at = (j & 1) * 2;
           if constexpr (ONE) {
-            f[0][(j & 1) * 2] = g == 0 ? h : g == 1 ? ll : 0u;
-            f[0][(j & 1) * 2 + 1] = g == 0 ? mm : 0u;
+            f[0][at] = g == 0 ? hi : g == 1 ? ll : 0u;
+            f[0][at + 1] = g == 0 ? mm : 0u;
+          } else if constexpr (WIDE) {
+            f[0][at + h] = hi;
+            f[AF - 2][at + h] = mm;
+            f[AF - 1][at + h] = ll;
           } else {
-            f[0][(j & 1) * 2] = h;
-            f[0][(j & 1) * 2 + 1] = mm;
-            f[AF - 1][(j & 1) * 2] = 0u;
-            f[AF - 1][(j & 1) * 2 + 1] = ll;
+            f[0][at] = hi;
+            f[0][at + 1] = mm;
+            f[AF - 1][at] = 0u;
+            f[AF - 1][at + 1] = ll;
           }
         }
-        l[nt] = l[nt] * corr[nt] + sum;
+        l[h] = l[h] * corr[h] + sum;
       }
       copies_wait_all_but_one();  // this unit's V
       // o = o corr + p V
@@ -891,7 +924,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
               v[mt][i] = *reinterpret_cast<const uint4*>(vp + (16 * mt + (i & 1) + (i >> 1) * 8) * PITCH + 128 * (F32 ? 2 * nb + hv : nb));
 #pragma unroll
           for (int e0 = 0; e0 < (F32 ? 4 : 8); e0 += EN) {
-            float c[NT][EN][4];
+            float c[EN][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               uint32_t b0[EN][SPL], b1[EN][SPL];
@@ -907,30 +940,39 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
                   split3(__uint_as_float(word_of(v[mt][2], e)), __uint_as_float(word_of(v[mt][3], e)), b1[i][0], b1[i][1], b1[i][2]);
                 }
               }
+              const uint32_t(&f)[AF][4] = pf[mt];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t(&f)[AF][4] = pf[nt][mt];
+              for (int t = SPL - 1; t >= 0; --t) {
 #pragma unroll
-                for (int t = SPL - 1; t >= 0; --t)
-#pragma unroll
-                  for (int i = 0; i < EN; ++i) {
-                    if (mt == 0 && t == SPL - 1) mma_bf16_first(c[nt][i], f[0], b0[i][t], b1[i][t]);
-                    else mma_bf16(c[nt][i], f[0], b0[i][t], b1[i][t]);
-                  }
-                if constexpr (!ONE) {
-#pragma unroll
-                  for (int i = 0; i < EN; ++i) mma_bf16(c[nt][i], f[AF - 1], b0[i][0], b1[i][0]);
+                for (int i = 0; i < EN; ++i) {
+                  if (mt == 0 && t == SPL - 1) mma_bf16_first(c[i], f[0], b0[i][t], b1[i][t]);
+                  else mma_bf16(c[i], f[0], b0[i][t], b1[i][t]);
                 }
+                if constexpr (WIDE) {
+                  if (t < 2) {
+#pragma unroll
+                    for (int i = 0; i < EN; ++i) mma_bf16(c[i], f[AF - 2], b0[i][t], b1[i][t]);
+                  }
+                }
+              }
+              if constexpr (!ONE) {
+#pragma unroll
+                for (int i = 0; i < EN; ++i) mma_bf16(c[i], f[AF - 1], b0[i][0], b1[i][0]);
               }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < EN; ++i) {
-                float(&d)[2] = o[nt][nb][4 * hv * (F32 ? 1 : 0) + e0 + i];
-                d[0] = fmaf(d[0], corr[nt], c[nt][i][0] + c[nt][i][2]);
-                d[1] = fmaf(d[1], corr[nt], c[nt][i][1] + c[nt][i][3]);
+            for (int i = 0; i < EN; ++i) {
+              float(&d)[QH][2] = o[nb][4 * hv + e0 + i];
+              if constexpr (WIDE) {
+                d[0][0] = fmaf(d[0][0], corr[0], c[i][0]);
+                d[0][1] = fmaf(d[0][1], corr[0], c[i][1]);
+                d[QH - 1][0] = fmaf(d[QH - 1][0], corr[QH - 1], c[i][2]);
+                d[QH - 1][1] = fmaf(d[QH - 1][1], corr[QH - 1], c[i][3]);
+              } else {
+                d[0][0] = fmaf(d[0][0], corr[0], c[i][0] + c[i][2]);
+                d[0][1] = fmaf(d[0][1], corr[0], c[i][1] + c[i][3]);
               }
+            }
           }
         }
       }
@@ -983,30 +1025,43 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, NTQ>::WARPS, PagedShap
     int n = 1, step = Shape::WARP_BYTES / 4;
     while (w + n < WARPS && warp_first(w + n) < min(end, chi)) ++n;
     const bool shared = i == 8 || end > chi;
-    float* dst = shared ? a.part + ((size_t)blockIdx.x * 2 + (i == 8 ? 0 : 1)) * PARTF : nullptr;
+    const int C = gridDim.x, mine = 2 * blockIdx.x + (i == 8 ? 0 : 1);
+    auto slot = [&](int s) { return a.part + (size_t)s * PARTF; };
+    float* dst = shared ? slot(mine) : nullptr;
+    const int c0 = shared ? cta_of(begin) : 0, ctas_of = shared ? cta_of(end - 1) - c0 + 1 : 1;
+    const bool two = ctas_of > PGA_JOIN;  // many CTAs: groups of PGA_JOIN join first, side by side
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int level = two ? 0 : 1; ; ++level) {
       combine(p0, p1, step, n, b, it, dst);
       if (!dst) break;
-      const int c0 = cta_of(begin);
-      n = cta_of(end - 1) - c0 + 1;
+      // the partial's group (all of the item's; of many, PGA_JOIN neighbours) and its counter
+      const int gr = two && level == 0 ? ((int)blockIdx.x - c0) / PGA_JOIN : 0;
+      const int head = 2 * (c0 + gr * PGA_JOIN) + (gr == 0 ? 1 : 0);  // the slot of the group's first: begun in c0, or not
+      n = !two ? ctas_of : level == 0 ? min(PGA_JOIN, ctas_of - gr * PGA_JOIN) : (ctas_of + PGA_JOIN - 1) / PGA_JOIN;
       __threadfence();
       sync();
-      int last = 0;
       if (first) {
-        last = atomicAdd(a.tick + c0, 1u) == (unsigned)(n - 1);
-        if (last) a.tick[c0] = 0;
+        unsigned* t = a.tick + (two && level == 1 ? 2 * C : 0) + head;
+        const bool last = atomicAdd(t, 1u) == (unsigned)(n - 1);
+        if (last) *t = 0;
         __threadfence();
         s_last[ONE ? warp : 0] = last;
       }
       sync();
-      last = s_last[ONE ? warp : 0];
+      const bool last = s_last[ONE ? warp : 0];
       sync();
       if (!last) break;
-      p0 = a.part + ((size_t)c0 * 2 + 1) * PARTF;  // begun in c0, carried on in the next CTAs
-      p1 = a.part + ((size_t)c0 + 1) * 2 * PARTF;
-      step = 2 * PARTF;
-      dst = nullptr;
+      if (two && level == 1) {  // the groups' sums, kept behind the CTAs' slots
+        p0 = slot(2 * C + head);
+        p1 = slot(2 * C + 2 * (c0 + PGA_JOIN));
+        step = 2 * PGA_JOIN * PARTF;
+        dst = nullptr;
+      } else {
+        p0 = slot(head);
+        p1 = slot((head & ~1) + 2);
+        step = 2 * PARTF;
+        dst = two ? slot(2 * C + head) : nullptr;
+      }
     }
   }
 }

@@ -23,8 +23,8 @@ struct PagedAttnArgs {
   const int32_t* head_count;
   float* out;                 // like q
   float* lse;                 // [B][rows][G] or nullptr
-  float* part;                // partials, two slots per CTA
-  unsigned* tick;             // one counter per CTA, zero between calls
+  float* part;                // partials: two slots per CTA, and as many for groups of CTAs
+  unsigned* tick;             // a counter per slot, zero between calls
   int* status;
   int B, W, rows, G, h_kv, dh, page, page_shift, n_pages, stride_rows, NQ;
   float scale_log2;
