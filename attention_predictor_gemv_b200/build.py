@@ -23,7 +23,8 @@ SOURCES = ["dv_api.cu", "dv_inst_legacy.cu", "dv_inst_legacy_attn.cu", "dv_inst_
            "dv_inst_q8.cu", "dv_paged.cu"]
 HEADERS = ["dv_common.cuh", "dv_kernels.cuh", "dv_fused.cuh", "dv_colowner.cuh", "dv_launch.cuh", "dv_launchers.cuh",
            "dv_api_kernels.cuh", "dv_stream.cuh", "dv_tc.cuh", "dv_tc_args.h",
-           "dv_tc_launch.h", "dv_paged.cuh", "dv_paged_launch.h"]
+           "dv_tc_launch.h", "dv_paged.cuh", "dv_paged_proj.cuh",
+           "dv_paged_launch.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

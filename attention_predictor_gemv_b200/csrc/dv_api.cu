@@ -978,7 +978,15 @@ dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, co
   int* status = at<int>(ws, L.status);
   float *q = at<float>(ws, L.q), *H = at<float>(ws, L.H);
   void *ks = at<char>(ws, P.ks), *vs = at<char>(ws, P.vs);
-  // the projections store k and v as into a cache of one slot
+  if (paged_proj_ok(B, d, wdtype, dh)) {
+    DV_TRY(run_paged_qkv(kv, Wqkv, bqkv, y, B, d, slots, head_idx, head_count, kh_max, exact_kv != 0, q, status, st));
+    if (kh_max > 0)
+      DV_TRY(run_paged_attn(kv, q, B, kh_max, 1, table, W, lens, scale, head_idx, head_count, H, nullptr,
+                            at<float>(ws, P.part), at<unsigned>(ws, L.attn_ctr), status, st));
+    return cuda_status(run_paged_wo(WOt, bO, H, B, d, h, dh, head_idx, head_count, kh_max, out, accumulate, status, st));
+  }
+  // fp32 weights, or more requests: the contiguous call's projections, which
+  // store k and v as into a cache of one slot
   const bool tc = tc_ok(B, d, wdtype, dh, 0);
   if (kh_max > 0) {
     if (tc)

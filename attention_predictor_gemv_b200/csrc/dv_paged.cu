@@ -1,6 +1,7 @@
 // Paged key-value cache: argument checks, launches and C entry points.
 // Declarations and argument contracts: include/dejavu.h.
 #include "dv_paged.cuh"
+#include "dv_paged_proj.cuh"
 #include "dv_launch.cuh"
 
 namespace dv {
@@ -117,6 +118,72 @@ cudaError_t run_paged_token(const dv_paged_kv* kv, const void* ks, const void* v
   const dim3 grid((unsigned)((vecs + PA_THREADS - 1) / PA_THREADS), (unsigned)B);
   return kv->kvdtype == DV_BF16 ? launch(paged_token_kernel<bf16>, grid, dim3(PA_THREADS), 0, st, a)
                                 : launch(paged_token_kernel<float>, grid, dim3(PA_THREADS), 0, st, a);
+}
+
+bool paged_proj_ok(int B, int d, dv_dtype wdtype, int dh) {
+  return wdtype == DV_BF16 && B <= PP_MAX_B && d % 8 == 0 && dh % 32 == 0;
+}
+
+cudaError_t run_paged_qkv(const dv_paged_kv* kv, const void* W, const float* bias, const float* y, int B, int d,
+                          const int32_t* slots, const int32_t* head_idx, const int32_t* head_count, int kh_max, int all,
+                          float* q, int* status, cudaStream_t st) {
+  PagedQkvArgs a = {};
+  a.W = static_cast<const bf16*>(W);
+  a.bias = bias;
+  a.y = y;
+  a.head_idx = head_idx;
+  a.head_count = head_count;
+  a.slots = slots;
+  a.q = q;
+  a.K = static_cast<bf16*>(kv->K);
+  a.V = static_cast<bf16*>(kv->V);
+  a.status = status;
+  a.B = B;
+  a.d = d;
+  a.h = kv->h_kv;
+  a.dh = kv->dh;
+  a.kh_max = kh_max;
+  a.all = all;
+  a.page = kv->page;
+  a.stride_rows = (int)stride_rows(kv);
+  a.n_slots = kv->n_pages * kv->page;
+  auto kern = B == 1 ? paged_qkv_kernel<1> : paged_qkv_kernel<8>;
+  cudaError_t e = allow_smem(kern, paged_qkv_smem());
+  if (e != cudaSuccess) return e;
+  return launch_main(kern, dim3(sm_count()), dim3(PP_THREADS), paged_qkv_smem(), st, a);
+}
+
+namespace {
+
+template <int QR, int NC>
+cudaError_t launch_wo(const PagedWoArgs& a, cudaStream_t st) {
+  using S = PagedWoShape<NC>;
+  const size_t smem = (size_t)PP_WARPS * S::SLOTS * S::SLOT;
+  cudaError_t e = allow_smem(paged_wo_kernel<QR, NC>, smem);
+  if (e != cudaSuccess) return e;
+  const int blocks = (a.d + S::CB - 1) / S::CB;
+  return launch_main(paged_wo_kernel<QR, NC>, dim3(blocks < sm_count() ? blocks : sm_count()), dim3(PP_THREADS), smem, st, a);
+}
+
+// Columns per CTA: the fewest (32-byte sectors whole) that give no more CTAs than SMs
+template <int QR>
+cudaError_t launch_wo_qr(const PagedWoArgs& a, cudaStream_t st) {
+  const int nc = ((a.d + sm_count() - 1) / sm_count() + 7) / 8;
+  if (nc <= 2) return launch_wo<QR, 2>(a, st);
+  if (nc <= 4) return launch_wo<QR, 4>(a, st);
+  if (nc <= 6) return launch_wo<QR, 6>(a, st);
+  if (nc <= 8) return launch_wo<QR, 8>(a, st);
+  if (nc <= 10) return launch_wo<QR, 10>(a, st);
+  return launch_wo<QR, 12>(a, st);
+}
+
+}  // namespace
+
+cudaError_t run_paged_wo(const void* W, const float* bias, const float* H, int B, int d, int h, int dh,
+                         const int32_t* head_idx, const int32_t* head_count, int kh_max, float* out, int accumulate,
+                         int* status, cudaStream_t st) {
+  PagedWoArgs a = {static_cast<const bf16*>(W), bias, H, head_idx, head_count, out, status, B, d, h, dh, kh_max, accumulate};
+  return B == 1 ? launch_wo_qr<1>(a, st) : launch_wo_qr<8>(a, st);
 }
 
 }  // namespace dv

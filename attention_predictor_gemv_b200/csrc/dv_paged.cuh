@@ -432,10 +432,10 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
   char* mine = smem_raw + warp * Shape::WARP_BYTES;
   auto part_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES + 2 * Shape::SLOT); };
   auto open_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES); };
-  griddep_launch();
   if (tid < 9) s_item[tid][0] = -1;
   __syncthreads();
   griddep_wait();
+  griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
 
   // units of every row, and their prefix sums
   const int cap = a.W * a.page;
@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
     }
   };
 
+  const uint32_t row0 = g == 0 ? ~0u : 0u, row1 = g == 1 ? ~0u : 0u;  // (masks: choices by row became branches)
   float o[NB][8][QH][2], m[QH], l[QH];  // (l: this lane's keys)
   uint32_t qa[NK][4], ql[ONE ? 1 : NK][2], qw[WIDE ? NK : 1][4];  // (WIDE: high, -, middle; low in ql and qx)
   uint32_t qx[WIDE ? NK : 1][2];
@@ -613,10 +614,10 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
         split3(x.x, x.y, hi.x, mm.x, ll.x);
         split3(x.z, x.w, hi.y, mm.y, ll.y);
         if constexpr (ONE) {
-          qa[s][0] = g == 0 ? hi.x : g == 1 ? ll.x : 0u;
-          qa[s][1] = g == 0 ? mm.x : 0u;
-          qa[s][2] = g == 0 ? hi.y : g == 1 ? ll.y : 0u;
-          qa[s][3] = g == 0 ? mm.y : 0u;
+          qa[s][0] = (hi.x & row0) | (ll.x & row1);
+          qa[s][1] = mm.x & row0;
+          qa[s][2] = (hi.y & row0) | (ll.y & row1);
+          qa[s][3] = mm.y & row0;
         } else if constexpr (WIDE) {
           qa[s][h] = hi.x;
           qa[s][2 + h] = hi.y;
@@ -894,8 +895,8 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
           uint32_t(&f)[AF][4] = pf[j >> 1];
           const int at = (j & 1) * 2;
           if constexpr (ONE) {
-            f[0][at] = g == 0 ? hi : g == 1 ? ll : 0u;
-            f[0][at + 1] = g == 0 ? mm : 0u;
+            f[0][at] = (hi & row0) | (ll & row1);
+            f[0][at + 1] = mm & row0;
           } else if constexpr (WIDE) {
             f[0][at + h] = hi;
             f[AF - 2][at + h] = mm;

@@ -43,5 +43,16 @@ cudaError_t run_paged_attn(const dv_paged_kv* kv, const float* q, int B, int row
 cudaError_t run_paged_token(const dv_paged_kv* kv, const void* ks, const void* vs, const int32_t* slots, int B,
                             const int32_t* head_idx, const int32_t* head_count, int kh_max, int all, float* out, int d,
                             int* status, cudaStream_t st);
+// The projections on mma.sync with fp32 operands in three bf16 terms: bf16
+// weights, at most 8 requests. q, k, v of the selected heads (k and v into
+// their pages, `all`: of every head; else the other heads' places cleared), and
+// W^O, which must follow the attention of this call's set on the stream.
+bool paged_proj_ok(int B, int d, dv_dtype wdtype, int dh);
+cudaError_t run_paged_qkv(const dv_paged_kv* kv, const void* W, const float* bias, const float* y, int B, int d,
+                          const int32_t* slots, const int32_t* head_idx, const int32_t* head_count, int kh_max, int all,
+                          float* q, int* status, cudaStream_t st);
+cudaError_t run_paged_wo(const void* W, const float* bias, const float* H, int B, int d, int h, int dh,
+                         const int32_t* head_idx, const int32_t* head_count, int kh_max, float* out, int accumulate,
+                         int* status, cudaStream_t st);
 
 }  // namespace dv

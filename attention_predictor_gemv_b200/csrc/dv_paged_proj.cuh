@@ -1,0 +1,422 @@
+// The projections of the head-sparse attention block over a paged cache, bf16
+// weights, up to 8 requests: q, k, v of the selected heads (k and v straight
+// into their pages) and W^O.
+//
+// Both stream weight rows once through shared memory (asynchronous 16-byte
+// copies, a ring per warp) into mma.sync m16n8k16 with the requests as rows:
+// the fp32 operand enters as three bf16 terms (dv_paged.cuh), so the products
+// are fp32's. The tensor core's sums are kept to one ring slot and added in
+// fp32 outside. The eight warps of a CTA share the products' long axis and add
+// their sums in warp order through shared memory: no atomics, results do not
+// depend on timing. Bound by reading the weights.
+#pragma once
+
+#include "dv_paged.cuh"
+
+namespace dv {
+
+constexpr int PP_WARPS = 8, PP_THREADS = 32 * PP_WARPS;
+constexpr int PP_MAX_B = 8;
+
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
+}
+
+// Two consecutive k slots of an operand row as A fragment words: rows 0-7 high
+// above middle terms (`a`), low terms in rows 8-15 of `b`; of one request
+// (ONE) high and middle in rows 0 and 8, low in row 1, all in `a`.
+template <bool ONE>
+__device__ __forceinline__ void a_words(float x, float y, int g, uint32_t& a_top, uint32_t& a_low, uint32_t& b_low) {
+  uint32_t h, m, l;
+  split3(x, y, h, m, l);
+  // (masks, not choices: a choice by row became branches, a warp's way through each of them)
+  const uint32_t row0 = g == 0 ? ~0u : 0u, row1 = g == 1 ? ~0u : 0u;
+  a_top = ONE ? (h & row0) | (l & row1) : h;
+  a_low = ONE ? m & row0 : m;
+  b_low = l;
+}
+
+// ----------------------------------------------------------------------------
+// q, k, v. Weight rows Wqkv[head][3][dh][d] of the selected heads (and, with
+// `all`, k and v of the others) form tiles of 8 rows; a CTA takes an equal
+// share of the tiles, up to four at a time, its warps a share of the d channels
+// each, 128 channels a ring slot. y lies in shared memory, a segment of the
+// channels at a time where it is larger than 64 KB: loaded from L2 within the
+// loop it queued behind the weights in flight (60 us against 26 us at 5376 rows
+// of 12288 channels). k and v are rounded into slots[b]; without
+// `all` the places of the other heads are cleared.
+// ----------------------------------------------------------------------------
+constexpr int PQ_TILES = 4, PQ_SLOTS = 2, PQ_PITCH = 256 + 16;
+constexpr int PQ_SLOT = PQ_TILES * 8 * PQ_PITCH;
+constexpr int PQ_STRIDE = 128 * PP_WARPS;                // channels that the warps take side by side
+constexpr int PQ_YF = 16384;                             // floats of y at a time
+constexpr int PQ_YPAD = 4;                               // of each request's row, in floats
+constexpr int PQ_MAX_TILES = 512;  // of a CTA: 3 * 1024 heads * 16 tiles over 100 SMs or more
+
+struct PagedQkvArgs {
+  const __nv_bfloat16* W;
+  const float* bias;
+  const float* y;
+  const int32_t *head_idx, *head_count;
+  const int32_t* slots;
+  float* q;  // [B][kh_max][dh]
+  __nv_bfloat16 *K, *V;
+  int* status;
+  int B, d, h, dh, kh_max, all, page, stride_rows, n_slots;
+};
+
+constexpr size_t PQ_RING = (size_t)PP_WARPS * PQ_SLOTS * PQ_SLOT;
+constexpr size_t paged_qkv_smem() { return PQ_RING + 4 * (PQ_YF + PP_MAX_B * PQ_YPAD); }
+static_assert(paged_qkv_smem() + 4 * PTK_MAX_H + PP_WARPS * PQ_TILES * 8 * 9 * 4 + 4 * PQ_MAX_TILES + 1024 <= 227 * 1024, "shared memory");
+
+template <int QR>
+__global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a) {
+  constexpr bool ONE = QR == 1;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ short s_head[PTK_MAX_H], s_rest[PTK_MAX_H];
+  __shared__ float red[PP_WARPS][PQ_TILES * 8][QR + (QR > 1)];
+  __shared__ int s_nrest, s_row[PQ_MAX_TILES];  // a tile's first weight row, -1: none
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  griddep_wait();
+  griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
+
+  // selected heads in order, -1 where out of range; the others in order
+  int nsel = *a.head_count;
+  if (nsel < 0 || nsel > a.kh_max) {
+    if (blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_CLAMPED);
+    nsel = nsel < 0 ? 0 : a.kh_max;
+  }
+  for (int i = tid; i < a.h; i += PP_THREADS) s_rest[i] = 0;
+  __syncthreads();
+  for (int j = tid; j < nsel; j += PP_THREADS) {
+    int head = a.head_idx[j];
+    if (head < 0 || head >= a.h) {
+      if (blockIdx.x == 0) raise_status(a.status, ST_RANGE);
+      head = -1;
+    } else {
+      s_rest[head] = 1;
+    }
+    s_head[j] = (short)head;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int i0 = 0; i0 < a.h; i0 += 32) {
+      const bool rest = i0 + lane < a.h && !s_rest[min(i0 + lane, a.h - 1)];
+      const unsigned in = __ballot_sync(0xffffffffu, rest);
+      __syncwarp();
+      if (rest) s_rest[n + __popc(in & ((1u << lane) - 1u))] = (short)(i0 + lane);  // (never past what was read)
+      __syncwarp();
+      n += __popc(in);
+    }
+    if (lane == 0) s_nrest = n;
+  }
+  __syncthreads();
+  const int per = a.dh >> 3;  // tiles of one head's q, k or v
+  const int sel_tiles = nsel * 3 * per, tiles = sel_tiles + (a.all ? s_nrest * 2 * per : 0);
+  const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x), t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
+
+  // A tile's place: its head (-1: none), which of q, k, v, first channel, place in the set
+  struct Tile { int head, m, c, j; };
+  auto tile_at = [&](int t) {
+    Tile p;
+    if (t < sel_tiles) {
+      p.j = t / (3 * per);
+      const int r = t - p.j * 3 * per;
+      p.m = r / per;
+      p.c = (r - p.m * per) * 8;
+      p.head = s_head[p.j];
+    } else {
+      const int u = t - sel_tiles, i = u / (2 * per), r = u - i * 2 * per;
+      p.j = -1;
+      p.m = 1 + r / per;
+      p.c = (r - (p.m - 1) * per) * 8;
+      p.head = s_rest[i];
+    }
+    return p;
+  };
+
+  for (int t = t0 + tid; t < t1; t += PP_THREADS) {
+    const Tile p = tile_at(t);
+    s_row[t - t0] = p.head < 0 ? -1 : (p.head * 3 + p.m) * a.dh + p.c;
+  }
+  __syncthreads();
+  if (t1 > t0) {
+    const int passes = (t1 - t0 + PQ_TILES - 1) / PQ_TILES, nt = (t1 - t0 + passes - 1) / passes;
+    const int blocks = (a.d + 127) >> 7;
+    const int nk = (blocks + PP_WARPS - 1 - warp) / PP_WARPS;  // blocks warp, warp + 8, ...: side by side in a row
+    const int units = passes * nk;
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring) + warp * PQ_SLOTS * PQ_SLOT + (lane >> 4) * PQ_PITCH + (lane & 15) * 16;
+    const char* mine = ring + warp * PQ_SLOTS * PQ_SLOT;
+    auto request = [&](int u) {
+      if (u < units) {
+        const int pass = u / nk, k = warp + (u - pass * nk) * PP_WARPS;
+        const int ch = k * 128 + (lane & 15) * 8;
+        const uint32_t to = at + (u % PQ_SLOTS) * PQ_SLOT;
+#pragma unroll
+        for (int i = 0; i < PQ_TILES; ++i) {
+          const int t = t0 + pass * nt + i;
+          if (i < nt && t < t1) {
+            const int row = s_row[t - t0];
+            const bool on = row >= 0 && ch < a.d;
+            const __nv_bfloat16* src = a.W + (on ? (size_t)(row + (lane >> 4)) * a.d + ch : 0);
+#pragma unroll
+            for (int r = 0; r < 8; r += 2) copy16_or_zero(to + (8 * i + r) * PQ_PITCH, src + (on ? (size_t)r * a.d : 0), on);
+          }
+        }
+      }
+      copies_commit();
+    };
+    float* s_y = reinterpret_cast<float*>(ring + PQ_RING);
+    const int seg = min((a.d + PQ_STRIDE - 1) / PQ_STRIDE, PQ_YF / PQ_STRIDE / a.B);  // strides at a time
+    const int pitch = seg * PQ_STRIDE + PQ_YPAD;
+#pragma unroll
+    for (int u = 0; u < PQ_SLOTS - 1; ++u) request(u);
+    for (int pass = 0; pass < passes; ++pass) {
+      float acc[PQ_TILES][2] = {};
+      for (int i0 = 0; i0 * PQ_STRIDE < a.d; i0 += seg) {
+        if (pass == 0 || seg * PQ_STRIDE < a.d) {
+          __syncthreads();
+          const int n4 = min(seg * PQ_STRIDE, a.d - i0 * PQ_STRIDE) >> 2;
+          for (int b = 0; b < a.B; ++b)
+            for (int i = tid; i < seg * PQ_STRIDE / 4; i += PP_THREADS)
+              reinterpret_cast<float4*>(s_y + b * pitch)[i] =
+                  i < n4 ? reinterpret_cast<const float4*>(a.y + (size_t)b * a.d + i0 * PQ_STRIDE)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+          __syncthreads();
+        }
+#pragma unroll 1
+      for (int k = i0; k < min(nk, i0 + seg); ++k) {
+        const int u = pass * nk + k;
+        request(u + PQ_SLOTS - 1);
+        uint32_t fa[8][4], fb[8][2];
+        const float* yp = s_y + (ONE ? 0 : g) * pitch + (k - i0) * PQ_STRIDE + warp * 128 + 16 * t4;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (ONE || g < a.B) x = *reinterpret_cast<const float4*>(yp + 64 * (s >> 2) + 4 * (s & 3));
+          a_words<ONE>(x.x, x.y, g, fa[s][0], fa[s][1], fb[s][0]);
+          a_words<ONE>(x.z, x.w, g, fa[s][2], fa[s][3], fb[s][1]);
+        }
+        copies_wait<PQ_SLOTS - 1>();
+        const char* w = mine + (u % PQ_SLOTS) * PQ_SLOT + g * PQ_PITCH + t4 * 32;
+        float c[PQ_TILES][4];
+#pragma unroll
+        for (int piece = 0; piece < 4; ++piece) {
+          uint4 v[PQ_TILES];
+#pragma unroll
+          for (int i = 0; i < PQ_TILES; ++i) v[i] = *reinterpret_cast<const uint4*>(w + 8 * i * PQ_PITCH + (piece >> 1) * 128 + (piece & 1) * 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int s = 2 * piece + h;
+#pragma unroll
+            for (int i = 0; i < PQ_TILES; ++i) {
+              const uint32_t b0 = h ? v[i].z : v[i].x, b1 = h ? v[i].w : v[i].y;
+              if (s == 0) mma_bf16_first(c[i], fa[s], b0, b1);
+              else mma_bf16(c[i], fa[s], b0, b1);
+            }
+            if constexpr (!ONE) {
+              const uint32_t low[4] = {0u, fb[s][0], 0u, fb[s][1]};
+#pragma unroll
+              for (int i = 0; i < PQ_TILES; ++i) mma_bf16(c[i], low, h ? v[i].z : v[i].x, h ? v[i].w : v[i].y);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < PQ_TILES; ++i) {
+          acc[i][0] += c[i][0] + c[i][2];
+          acc[i][1] += c[i][1] + c[i][3];
+        }
+        __syncwarp();  // the slot is free
+      }
+      }
+      if (pass > 0) __syncthreads();  // (the last pass's sums are read)
+#pragma unroll
+      for (int i = 0; i < PQ_TILES; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = acc[i][e];
+          if constexpr (ONE) v += __shfl_xor_sync(0xffffffffu, v, 4);
+          if (!ONE || g == 0) red[warp][8 * i + 2 * t4 + e][ONE ? 0 : g] = v;
+        }
+      __syncthreads();
+      if (tid < PQ_TILES * 8 * QR) {
+        const int r = tid % (PQ_TILES * 8), b = tid / (PQ_TILES * 8), i = r >> 3, t = t0 + pass * nt + i;
+        if (i < nt && t < t1 && b < a.B) {
+          const Tile p = tile_at(t);
+          if (p.head >= 0) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < PP_WARPS; ++w) v += red[w][r][b];
+            const int c = p.c + (r & 7);
+            if (a.bias) v += a.bias[(size_t)(p.head * 3 + p.m) * a.dh + c];
+            if (p.m == 0) {
+              a.q[((size_t)b * a.kh_max + p.j) * a.dh + c] = v;
+            } else {
+              const int slot = a.slots[b];
+              if (slot >= 0 && slot < a.n_slots) {
+                const int pg = slot / a.page;
+                const long long row = (long long)pg * a.stride_rows + p.head * a.page + (slot - pg * a.page);
+                (p.m == 1 ? a.K : a.V)[row * a.dh + c] = __float2bfloat16_rn(v);
+              } else if (slot >= 0) {
+                raise_status(a.status, ST_RANGE);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  if (!a.all) {
+    const int n = s_nrest * a.B, vecs = a.dh >> 3;  // (head, request) pairs, 16-byte vectors of each
+    for (int x = blockIdx.x * PP_THREADS + tid; x < n * vecs; x += gridDim.x * PP_THREADS) {
+      const int pr = x / vecs, v = x - pr * vecs, b = pr % a.B, head = s_rest[pr / a.B];
+      const int slot = a.slots[b];
+      if (slot < 0 || slot >= a.n_slots) {
+        if (slot >= 0) raise_status(a.status, ST_RANGE);
+        continue;
+      }
+      const int pg = slot / a.page;
+      const long long row = (long long)pg * a.stride_rows + head * a.page + (slot - pg * a.page);
+      reinterpret_cast<uint4*>(a.K)[row * vecs + v] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(a.V)[row * vecs + v] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// W^O: out[b][c] (+)= sum_r H[b][r] WOt[row r][c] (+ bO[c]) over the rows of
+// the selected heads. A CTA takes 8 NC columns and all rows, its warps a share
+// of the rows each, 32 rows a ring slot; the weights are the MMA's columns,
+// read by transposing matrix loads. The ring is filled before the wait for the
+// attention, which writes H alone.
+// ----------------------------------------------------------------------------
+struct PagedWoArgs {
+  const __nv_bfloat16* W;
+  const float* bias;
+  const float* H;  // [B][kh_max][dh]
+  const int32_t *head_idx, *head_count;
+  float* out;
+  int* status;
+  int B, d, h, dh, kh_max, accumulate;
+};
+
+template <int NC>
+struct PagedWoShape {
+  static constexpr int CB = 8 * NC, PITCH = 2 * CB + 16, SLOT = 32 * PITCH;
+  static constexpr int FIT = 200 * 1024 / (PP_WARPS * SLOT), SLOTS = FIT < 6 ? FIT : 6;
+  static_assert(SLOTS >= 2 && PP_WARPS * SLOTS * SLOT >= PP_WARPS * 8 * CB * 4, "the ring holds the warps' sums at the end");
+};
+
+template <int QR, int NC>
+__global__ void __launch_bounds__(PP_THREADS, 1) paged_wo_kernel(PagedWoArgs a) {
+  constexpr bool ONE = QR == 1;
+  using S = PagedWoShape<NC>;
+  constexpr int CB = S::CB, PITCH = S::PITCH, SLOTS = S::SLOTS, PIECES = CB / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(16) char ring[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  int nsel = *a.head_count;
+  nsel = nsel < 0 ? 0 : min(nsel, a.kh_max);
+  const int per = a.dh >> 5, nu = nsel * per;  // units of 32 rows
+  const int ulo = nu * warp / PP_WARPS, units = nu * (warp + 1) / PP_WARPS - ulo;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * SLOTS * S::SLOT;
+  bool waited = false;
+  for (int c0 = blockIdx.x * CB; c0 < a.d; c0 += gridDim.x * CB) {
+    auto request = [&](int u) {
+      if (u < units) {
+        const int j = (ulo + u) / per, head = a.head_idx[j];
+        const bool good = head >= 0 && head < a.h;
+        const __nv_bfloat16* src = a.W + (good ? ((size_t)head * a.dh + (ulo + u - j * per) * 32) * a.d + c0 : 0);
+        const uint32_t to = base + (u % SLOTS) * S::SLOT;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int e = i * 32 + lane, r = e / PIECES, c = e - r * PIECES;
+          const bool on = good && c0 + 8 * c < a.d;
+          copy16_or_zero(to + r * PITCH + c * 16, src + (on ? (size_t)r * a.d + 8 * c : 0), on);
+        }
+      }
+      copies_commit();
+    };
+#pragma unroll
+    for (int u = 0; u < SLOTS - 1; ++u) request(u);
+    if (!waited) griddep_wait(), waited = true;  // H, and the last readers and writers of out
+    // H of a unit: two steps of 16 rows, slots 2 t, + 1, + 8, + 9 of each
+    auto load_h = [&](int u, float2 (&x)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = make_float2(0.f, 0.f);
+        if (ONE || g < a.B)
+          x[i] = __ldcg(reinterpret_cast<const float2*>(a.H + (size_t)(ONE ? 0 : g) * a.kh_max * a.dh + (ulo + u) * 32 + 16 * (i >> 1) + 8 * (i & 1) + 2 * t4));
+      }
+    };
+    float acc[NC][2] = {};
+    float2 x[4];
+    if (units > 0) load_h(0, x);
+#pragma unroll 1
+    for (int u = 0; u < units; ++u) {
+      request(u + SLOTS - 1);
+      uint32_t fa[2][4], fb[2][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a_words<ONE>(x[i].x, x[i].y, g, fa[i >> 1][2 * (i & 1)], fa[i >> 1][2 * (i & 1) + 1], fb[i >> 1][i & 1]);
+      if (u + 1 < units) load_h(u + 1, x);
+      copies_wait<SLOTS - 1>();
+      const uint32_t w = base + (u % SLOTS) * S::SLOT + ((lane >> 3 & 1) * 8 + (lane & 7)) * PITCH + (lane >> 4) * 16;
+#pragma unroll
+      for (int n = 0; n < NC; n += 2) {
+        float c[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t b[4];
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                       : "r"(w + 16 * k * PITCH + n * 16)
+                       : "memory");
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (k == 0) mma_bf16_first(c[i], fa[k], b[2 * i], b[2 * i + 1]);
+            else mma_bf16(c[i], fa[k], b[2 * i], b[2 * i + 1]);
+          }
+          if constexpr (!ONE) {
+            const uint32_t low[4] = {0u, fb[k][0], 0u, fb[k][1]};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mma_bf16(c[i], low, b[2 * i], b[2 * i + 1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc[n + i][0] += c[i][0] + c[i][2];
+          acc[n + i][1] += c[i][1] + c[i][3];
+        }
+      }
+      __syncwarp();  // the slot is free
+    }
+    copies_wait<0>();
+    __syncthreads();  // the rings are free
+    float* red = reinterpret_cast<float*>(ring);  // [warps][QR][CB]
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = acc[n][e];
+        if constexpr (ONE) v += __shfl_xor_sync(0xffffffffu, v, 4);
+        if (!ONE || g == 0) red[(warp * QR + (ONE ? 0 : g)) * CB + 8 * n + 2 * t4 + e] = v;
+      }
+    __syncthreads();
+    for (int i = tid; i < a.B * CB; i += PP_THREADS) {
+      const int b = i / CB, c = i - b * CB;
+      if (c0 + c >= a.d) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < PP_WARPS; ++w) v += red[(w * QR + b) * CB + c];
+      if (a.bias) v += a.bias[c0 + c];
+      float* o = a.out + (size_t)b * a.d + c0 + c;
+      *o = a.accumulate ? *o + v : v;
+    }
+    __syncthreads();
+  }
+  if (!waited) griddep_wait();
+  griddep_launch();
+}
+
+}  // namespace dv
