@@ -982,7 +982,7 @@ dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, co
     DV_TRY(run_paged_qkv(kv, Wqkv, bqkv, y, B, d, slots, head_idx, head_count, kh_max, exact_kv != 0, q, status, st));
     if (kh_max > 0)
       DV_TRY(run_paged_attn(kv, q, B, kh_max, 1, table, W, lens, scale, head_idx, head_count, H, nullptr,
-                            at<float>(ws, P.part), at<unsigned>(ws, L.attn_ctr), status, st));
+                            at<float>(ws, P.part), at<unsigned>(ws, L.attn_ctr), status, st, true));
     return cuda_status(run_paged_wo(WOt, bO, H, B, d, h, dh, head_idx, head_count, kh_max, out, accumulate, status, st));
   }
   // fp32 weights, or more requests: the contiguous call's projections, which

@@ -65,8 +65,9 @@ dv_status paged_kv_check(const dv_paged_kv* kv) {
 
 cudaError_t run_paged_attn(const dv_paged_kv* kv, const float* q, int B, int rows, int G, const int32_t* table, int W,
                            const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
-                           float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st) {
+                           float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st, bool early) {
   PagedAttnArgs a = {};
+  a.early = early;
   a.q = q;
   a.K = kv->K;
   a.V = kv->V;

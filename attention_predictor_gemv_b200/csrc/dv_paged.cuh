@@ -434,8 +434,10 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
   auto open_of = [&](int w) { return reinterpret_cast<float*>(smem_raw + w * Shape::WARP_BYTES); };
   if (tid < 9) s_item[tid][0] = -1;
   __syncthreads();
-  griddep_wait();
-  griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
+  // `early`: what this call reads before its q was written before the kernel that writes q began (that one lets this
+  // start only after its own wait), so only q and the new tokens' rows are waited for, further down
+  if (!a.early) griddep_wait();
+  griddep_launch();
 
   // units of every row, and their prefix sums
   const int cap = a.W * a.page;
@@ -475,13 +477,6 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
     if (tid == 0) s_pre[a.B] = units;
     __syncthreads();
   }
-  // rows without keys: zeros (and minus infinity)
-  for (int r = blockIdx.x; r < a.B; r += gridDim.x) {
-    if (s_pre[r + 1] > s_pre[r]) continue;
-    for (int i = tid; i < nh * a.G * a.dh; i += THREADS) a.out[(size_t)r * HR * a.dh + i] = 0.f;
-    if (a.lse)
-      for (int i = tid; i < nh * a.G; i += THREADS) a.lse[(size_t)r * HR + i] = -INFINITY;
-  }
   const int IR = nh * a.NQ;     // items of a row
   const int U = units * IR;     // (below 2^31: checked on the host for the largest lengths)
   // CTA c takes the units from cta_first(c) on, its warps equal stretches of them. Rows of one length: each CTA has whole
@@ -499,7 +494,20 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
       if (per > 0 && (same + WARPS * per - 1) / (WARPS * per) * 16 <= even * 17) group = same, ctas = per, CE = items * per;
     }
   }
-  if ((int)blockIdx.x >= CE) return;
+  // rows without keys: zeros (and minus infinity)
+  auto empty_rows = [&]() {
+    for (int r = blockIdx.x; r < a.B; r += gridDim.x) {
+      if (s_pre[r + 1] > s_pre[r]) continue;
+      for (int i = tid; i < nh * a.G * a.dh; i += THREADS) a.out[(size_t)r * HR * a.dh + i] = 0.f;
+      if (a.lse)
+        for (int i = tid; i < nh * a.G; i += THREADS) a.lse[(size_t)r * HR + i] = -INFINITY;
+    }
+  };
+  if ((int)blockIdx.x >= CE) {
+    if (a.early) griddep_wait();
+    empty_rows();
+    return;
+  }
   const int each = group / ctas, extra = group - each * ctas;
   auto cta_first = [&](int c) {
     const int gr = c / ctas, p = c - gr * ctas;
@@ -760,6 +768,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
     }
   };
 
+  if (wlo >= whi && a.early) griddep_wait();
   if (wlo < whi) {
     PagedAt cur = locate(wlo);
     if (warp == 0 && lane == 0 && cur.t > 0) {
@@ -772,6 +781,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
     const int count = whi - wlo;
     int row = pool_row(cur);
     unsigned in = __ballot_sync(0xffffffffu, row >= 0);
+    if (a.early) griddep_wait();
     stage_q(cur);
     request(a.K, slot_at, row, in);
     copies_commit();
@@ -1008,6 +1018,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
       }
     }
   }
+  empty_rows();
   __syncthreads();
 
   // What crosses warps: item by item, its partials in the order of their warps; by all warps, items of one query by a

@@ -28,6 +28,7 @@ struct PagedAttnArgs {
   int* status;
   int B, W, rows, G, h_kv, dh, page, page_shift, n_pages, stride_rows, NQ;
   float scale_log2;
+  int early;                  // the kernel before on the stream is this call's paged_qkv_kernel
 };
 
 // Floats of partial slots the attention needs for heads of dh channels.
@@ -36,7 +37,7 @@ size_t paged_attn_part_floats(int dh);
 dv_status paged_kv_check(const dv_paged_kv* kv);
 cudaError_t run_paged_attn(const dv_paged_kv* kv, const float* q, int B, int rows, int G, const int32_t* table, int W,
                            const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
-                           float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st);
+                           float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st, bool early = false);
 // One new token per request: its k, v of every head from the staging rows
 // ks, vs [B][h][dh] (the cache's dtype) into slots[b]; heads outside the set
 // get zeros unless `all`. Also clears out [B][d] when it is given.

@@ -82,6 +82,20 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
   griddep_wait();
   griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
 
+  // y, a segment of the channels, on its way to shared memory; channels past d become zeros
+  float* s_y = reinterpret_cast<float*>(ring + PQ_RING);
+  const int seg = min((a.d + PQ_STRIDE - 1) / PQ_STRIDE, PQ_YF / PQ_STRIDE / a.B);  // strides of channels at a time
+  const int pitch = seg * PQ_STRIDE + PQ_YPAD;
+  auto request_y = [&](int i0) {
+    const int n4 = min(seg * PQ_STRIDE, a.d - i0 * PQ_STRIDE) >> 2;
+    for (int b = 0; b < a.B; ++b)
+      for (int i = tid; i < seg * PQ_STRIDE / 4; i += PP_THREADS)
+        copy16_or_zero((uint32_t)__cvta_generic_to_shared(s_y + b * pitch + 4 * i),
+                       a.y + (i < n4 ? (size_t)b * a.d + i0 * PQ_STRIDE + 4 * i : 0), i < n4);
+    copies_commit();
+  };
+  request_y(0);
+
   // selected heads in order, -1 where out of range; the others in order
   int nsel = *a.head_count;
   if (nsel < 0 || nsel > a.kh_max) {
@@ -169,21 +183,18 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
       }
       copies_commit();
     };
-    float* s_y = reinterpret_cast<float*>(ring + PQ_RING);
-    const int seg = min((a.d + PQ_STRIDE - 1) / PQ_STRIDE, PQ_YF / PQ_STRIDE / a.B);  // strides at a time
-    const int pitch = seg * PQ_STRIDE + PQ_YPAD;
 #pragma unroll
     for (int u = 0; u < PQ_SLOTS - 1; ++u) request(u);
     for (int pass = 0; pass < passes; ++pass) {
       float acc[PQ_TILES][2] = {};
       for (int i0 = 0; i0 * PQ_STRIDE < a.d; i0 += seg) {
-        if (pass == 0 || seg * PQ_STRIDE < a.d) {
+        if (pass + i0 == 0) {  // the first segment: all but the ring's groups
+          copies_wait<PQ_SLOTS - 1>();
           __syncthreads();
-          const int n4 = min(seg * PQ_STRIDE, a.d - i0 * PQ_STRIDE) >> 2;
-          for (int b = 0; b < a.B; ++b)
-            for (int i = tid; i < seg * PQ_STRIDE / 4; i += PP_THREADS)
-              reinterpret_cast<float4*>(s_y + b * pitch)[i] =
-                  i < n4 ? reinterpret_cast<const float4*>(a.y + (size_t)b * a.d + i0 * PQ_STRIDE)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (seg * PQ_STRIDE < a.d) {
+          __syncthreads();
+          request_y(i0);
+          copies_wait<0>();
           __syncthreads();
         }
 #pragma unroll 1
@@ -304,7 +315,8 @@ struct PagedWoArgs {
 
 template <int NC>
 struct PagedWoShape {
-  static constexpr int CB = 8 * NC, PITCH = 2 * CB + 16, SLOT = 32 * PITCH;
+  static constexpr int CB = 8 * NC, PITCH = 2 * CB + 16, HPITCH = 36;  // (floats; rows of H in other banks)
+  static constexpr int ROWS = 32 * PITCH, SLOT = ROWS + PP_MAX_B * HPITCH * 4;
   static constexpr int FIT = 200 * 1024 / (PP_WARPS * SLOT), SLOTS = FIT < 6 ? FIT : 6;
   static_assert(SLOTS >= 2 && PP_WARPS * SLOTS * SLOT >= PP_WARPS * 8 * CB * 4, "the ring holds the warps' sums at the end");
 };
@@ -336,31 +348,40 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_wo_kernel(PagedWoArgs a) 
           copy16_or_zero(to + r * PITCH + c * 16, src + (on ? (size_t)r * a.d + 8 * c : 0), on);
         }
       }
+    };
+    // H of its rows, [B][32]
+    auto request_h = [&](int u) {
+      if (u < units)
+        for (int i = lane; i < 8 * a.B; i += 32)
+          copy16(base + (u % SLOTS) * S::SLOT + S::ROWS + ((i >> 3) * S::HPITCH + 4 * (i & 7)) * 4,
+                 a.H + (size_t)(i >> 3) * a.kh_max * a.dh + (ulo + u) * 32 + 4 * (i & 7));
+    };
+#pragma unroll
+    for (int u = 0; u < SLOTS - 1; ++u) {
+      request(u);
       copies_commit();
-    };
-#pragma unroll
-    for (int u = 0; u < SLOTS - 1; ++u) request(u);
+    }
     if (!waited) griddep_wait(), waited = true;  // H, and the last readers and writers of out
-    // H of a unit: two steps of 16 rows, slots 2 t, + 1, + 8, + 9 of each
-    auto load_h = [&](int u, float2 (&x)[4]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = make_float2(0.f, 0.f);
-        if (ONE || g < a.B)
-          x[i] = __ldcg(reinterpret_cast<const float2*>(a.H + (size_t)(ONE ? 0 : g) * a.kh_max * a.dh + (ulo + u) * 32 + 16 * (i >> 1) + 8 * (i & 1) + 2 * t4));
-      }
-    };
+    for (int u = 0; u < SLOTS - 1; ++u) request_h(u);
+    copies_commit();
     float acc[NC][2] = {};
-    float2 x[4];
-    if (units > 0) load_h(0, x);
 #pragma unroll 1
     for (int u = 0; u < units; ++u) {
       request(u + SLOTS - 1);
+      request_h(u + SLOTS - 1);
+      copies_commit();
+      if (u == 0) copies_wait<1>();  // (H of the first slots came last)
+      else copies_wait<SLOTS - 1>();
+      // two steps of 16 rows, k slots 2 t, + 1, + 8, + 9 of each
       uint32_t fa[2][4], fb[2][2];
+      const float* hp = reinterpret_cast<const float*>(ring + (warp * SLOTS + u % SLOTS) * S::SLOT + S::ROWS) + (ONE ? 0 : g) * S::HPITCH + 2 * t4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a_words<ONE>(x[i].x, x[i].y, g, fa[i >> 1][2 * (i & 1)], fa[i >> 1][2 * (i & 1) + 1], fb[i >> 1][i & 1]);
-      if (u + 1 < units) load_h(u + 1, x);
-      copies_wait<SLOTS - 1>();
+      for (int i = 0; i < 4; ++i) {
+        float2 x = make_float2(0.f, 0.f);
+        if (ONE || g < a.B) x = *reinterpret_cast<const float2*>(hp + 8 * i);
+        a_words<ONE>(x.x, x.y, g, fa[i >> 1][2 * (i & 1)], fa[i >> 1][2 * (i & 1) + 1], fb[i >> 1][i & 1]);
+      }
       const uint32_t w = base + (u % SLOTS) * S::SLOT + ((lane >> 3 & 1) * 8 + (lane & 7)) * PITCH + (lane >> 4) * 16;
 #pragma unroll
       for (int n = 0; n < NC; n += 2) {
