@@ -50,10 +50,12 @@ __device__ __forceinline__ unsigned cluster_size() {
 // when the running sums of pages and of tokens up to it are covered, so the
 // decision is three prefix sums over the rows.
 //
-// One cluster does a call: every CTA forms the prefix sums of all rows for
-// itself (at most 4096 rows, 8 bytes each from L2), so the only exchange is one
-// cluster barrier between the pushes onto the stack and the takes from it.
-// Bound by latency: launch, the scans, three dependent loads.
+// One cluster does that: every CTA forms the prefix sums of all rows for itself
+// (at most 4096 rows, 8 bytes each from L2; one scan of all three sums, a second
+// only where a request is refused), so the only exchange is one cluster barrier
+// between the pushes onto the stack and the takes from it. Many tokens' slots
+// are written by a second kernel over all SMs (page_slots_kernel). Bound by
+// latency: launch, scan, three dependent loads.
 // ----------------------------------------------------------------------------
 constexpr int PT_THREADS = 1024;
 
@@ -72,16 +74,48 @@ struct PageTablesArgs {
   int R, W, page, n_pages, T;
 };
 
+struct PtSums {
+  unsigned gone, need, add;  // pages given back, pages wanted, tokens added
+};
+
+// Exclusive prefix sums of three values over the block, and their totals
+__device__ __forceinline__ PtSums pt_scan(PtSums v, PtSums (&sc)[33], PtSums& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  auto warp_scan = [&](PtSums x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned a = __shfl_up_sync(0xffffffffu, x.gone, o), b = __shfl_up_sync(0xffffffffu, x.need, o),
+                     c = __shfl_up_sync(0xffffffffu, x.add, o);
+      if (lane >= o) x.gone += a, x.need += b, x.add += c;
+    }
+    return x;
+  };
+  const PtSums in = warp_scan(v);
+  if (lane == 31) sc[w] = in;
+  __syncthreads();
+  if (w == 0) {
+    const PtSums x = sc[lane], y = warp_scan(x);
+    sc[lane] = {y.gone - x.gone, y.need - x.need, y.add - x.add};
+    if (lane == 31) sc[32] = y;
+  }
+  __syncthreads();
+  total = sc[32];
+  const PtSums b = sc[w];
+  __syncthreads();
+  return {b.gone + in.gone - v.gone, b.need + in.need - v.need, b.add + in.add - v.add};
+}
+
 __global__ void __launch_bounds__(PT_THREADS) page_tables_kernel(PageTablesArgs a) {
   extern __shared__ int sm[];
-  __shared__ unsigned sc[PT_THREADS / 32 + 1];
+  __shared__ PtSums sc[33];
+  static_assert(PT_THREADS == 1024, "a warp scans the warps' sums");
   const int R = a.R, tid = threadIdx.x;
   int* s_len = sm;               // current lengths
   int* s_free = s_len + R + 1;   // prefix of pages given back
   int* s_need = s_free + R + 1;  // prefix of pages taken
   int* s_tok = s_need + R + 1;   // prefix of tokens added
-  griddep_launch();
   griddep_wait();
+  griddep_launch();  // (after the wait: the slots' kernel starts early)
   const int cap = a.W * a.page;
   int bad = 0;
   int fc = *a.free_count;
@@ -89,57 +123,72 @@ __global__ void __launch_bounds__(PT_THREADS) page_tables_kernel(PageTablesArgs 
     fc = fc < 0 ? 0 : a.n_pages;
     bad |= ST_RANGE;
   }
-  unsigned base = 0;
-  for (int r0 = 0; r0 < R; r0 += PT_THREADS) {
-    const int r = r0 + tid;
-    unsigned gone = 0;
-    if (r < R) {
-      const int len = a.lens[r], want = a.want[r];
-      s_len[r] = len;
-      if (len < 0 || len > cap) bad |= ST_RANGE;
-      else if (want >= 0 && want < len) gone = (len + a.page - 1) / a.page - (want + a.page - 1) / a.page;
+  auto pages = [&](int n) { return (n + a.page - 1) / a.page; };
+  // a row's wishes; whether its lengths are within its table
+  auto wishes = [&](int len, int want, bool& fits) {
+    PtSums v = {0u, 0u, 0u};
+    fits = len >= 0 && len <= cap && want <= cap;
+    if (fits && want >= 0) {
+      if (want < len) v.gone = pages(len) - pages(want);
+      else v.need = pages(want) - pages(len), v.add = want - len;
     }
-    unsigned tot;
-    const unsigned ex = block_exclusive_scan<PT_THREADS>(gone, sc, &tot);
-    if (r < R) s_free[r] = base + ex;
-    base += tot;
-  }
-  if (tid == 0) s_free[R] = base;
-  const int F = (int)base;
-  const int avail = min(fc + F, a.n_pages);
-  if (fc + F > a.n_pages) bad |= ST_RANGE;
-  unsigned need_all = 0, tok_all = 0, need_ok = 0, tok_ok = 0;
+    return v;
+  };
+  PtSums sum = {0u, 0u, 0u};
+  bool all_fit = true;
   for (int r0 = 0; r0 < R; r0 += PT_THREADS) {
     const int r = r0 + tid;
-    unsigned need = 0, add = 0;
+    PtSums v = {0u, 0u, 0u}, tot;
     bool fits = true;
     if (r < R) {
-      const int len = s_len[r], want = a.want[r];
-      fits = len >= 0 && len <= cap && want <= cap;
-      if (fits && want > len) {
-        need = (want + a.page - 1) / a.page - (len + a.page - 1) / a.page;
-        add = want - len;
-      }
+      const int len = a.lens[r];
+      s_len[r] = len;
+      if (len < 0 || len > cap) bad |= ST_RANGE;
+      v = wishes(len, a.want[r], fits);
     }
-    unsigned nt, tt, n2, t2;
-    const unsigned ne = block_exclusive_scan<PT_THREADS>(need, sc, &nt);
-    const unsigned te = block_exclusive_scan<PT_THREADS>(add, sc, &tt);
-    const bool ok = fits && (need == 0 || need_all + ne + need <= (unsigned)avail) &&
-                    (add == 0 || tok_all + te + add <= (unsigned)a.T);
-    const unsigned ge = block_exclusive_scan<PT_THREADS>(ok ? need : 0u, sc, &n2);
-    const unsigned he = block_exclusive_scan<PT_THREADS>(ok ? add : 0u, sc, &t2);
+    all_fit &= fits;
+    const PtSums ex = pt_scan(v, sc, tot);
     if (r < R) {
-      s_need[r] = need_ok + ge;
-      s_tok[r] = tok_ok + he;
-      if (!ok) bad |= ST_REFUSED;
-      if (cluster_rank() == 0) a.granted[r] = ok;
+      s_free[r] = sum.gone + ex.gone;
+      s_need[r] = sum.need + ex.need;
+      s_tok[r] = sum.add + ex.add;
     }
-    need_all += nt;
-    tok_all += tt;
-    need_ok += n2;
-    tok_ok += t2;
+    sum = {sum.gone + tot.gone, sum.need + tot.need, sum.add + tot.add};
+  }
+  const int F = (int)sum.gone;
+  const int avail = min(fc + F, a.n_pages);
+  if (fc + F > a.n_pages) bad |= ST_RANGE;
+  unsigned need_ok = sum.need, tok_ok = sum.add;
+  if (__syncthreads_and(all_fit) && sum.need <= (unsigned)avail && sum.add <= (unsigned)a.T) {
+    if (cluster_rank() == 0)
+      for (int r = tid; r < R; r += PT_THREADS) a.granted[r] = 1;
+  } else {  // some request is refused: the prefix sums again, of those granted
+    need_ok = tok_ok = 0;
+    for (int r0 = 0; r0 < R; r0 += PT_THREADS) {
+      const int r = r0 + tid;
+      PtSums v = {0u, 0u, 0u}, tot;
+      bool ok = true;
+      if (r < R) {
+        v = wishes(s_len[r], a.want[r], ok);
+        v.gone = 0;
+        ok = ok && (v.need == 0 || s_need[r] + v.need <= (unsigned)avail) && (v.add == 0 || s_tok[r] + v.add <= (unsigned)a.T);
+        if (!ok) {
+          v.need = v.add = 0;
+          bad |= ST_REFUSED;
+        }
+        if (cluster_rank() == 0) a.granted[r] = ok;
+      }
+      const PtSums ex = pt_scan(v, sc, tot);
+      if (r < R) {
+        s_need[r] = need_ok + ex.need;
+        s_tok[r] = tok_ok + ex.add;
+      }
+      need_ok += tot.need;
+      tok_ok += tot.add;
+    }
   }
   if (tid == 0) {
+    s_free[R] = F;
     s_need[R] = need_ok;
     s_tok[R] = tok_ok;
   }
@@ -164,6 +213,9 @@ __global__ void __launch_bounds__(PT_THREADS) page_tables_kernel(PageTablesArgs 
     const int len = s_len[r], want = a.want[r];
     a.lens_out[r] = len >= 0 && len <= cap && want >= 0 && want < len ? want : len + (s_tok[r + 1] - s_tok[r]);
   }
+  if (gt == 0) *a.free_count_out = avail - (int)need_ok;
+  if (bad) raise_status(a.status, bad);
+  if (!a.slots) return;  // (page_slots_kernel's)
   // slots: four consecutive tokens a thread; a token's page is one just taken
   // (from the stack, not from the table another CTA writes) or an old one
   const int Tq = (a.T + 3) >> 2;
@@ -192,8 +244,43 @@ __global__ void __launch_bounds__(PT_THREADS) page_tables_kernel(PageTablesArgs 
         if (4 * i + e < a.T) a.slots[4 * i + e] = s[e];
     }
   }
-  if (gt == 0) *a.free_count_out = avail - (int)need_ok;
-  if (bad) raise_status(a.status, bad);
+}
+
+// The slots of many tokens, from the block tables and lengths just written:
+// four consecutive tokens a thread, their row found in the offsets.
+constexpr int PS_THREADS = 256;
+
+__global__ void __launch_bounds__(PS_THREADS)
+    page_slots_kernel(const int32_t* __restrict__ lens_out, const int32_t* __restrict__ table, const int32_t* __restrict__ offsets,
+                      int32_t* __restrict__ slots, int R, int W, int page, int T) {
+  extern __shared__ int s_tok[];
+  griddep_launch();
+  griddep_wait();
+  for (int r = threadIdx.x; r <= R; r += PS_THREADS) s_tok[r] = __ldcg(offsets + r);
+  __syncthreads();
+  const int tokens = s_tok[R];
+  for (int i = blockIdx.x * PS_THREADS + threadIdx.x; i < (T + 3) >> 2; i += gridDim.x * PS_THREADS) {
+    int s[4], r = -1, end = -1, old = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 4 * i + e;
+      s[e] = -1;
+      if (t >= tokens) continue;
+      if (t >= end) {
+        r = row_of(s_tok, R, t);
+        end = s_tok[r + 1];
+        old = __ldcg(lens_out + r) - end;  // the length after its last token, so a token's place is old + t
+      }
+      const int pos = old + t, pi = pos / page;
+      s[e] = __ldcg(table + (size_t)r * W + pi) * page + (pos - pi * page);
+    }
+    if (4 * i + 3 < T) {
+      *reinterpret_cast<int4*>(slots + 4 * i) = make_int4(s[0], s[1], s[2], s[3]);
+    } else {
+      for (int e = 0; e < 4; ++e)
+        if (4 * i + e < T) slots[4 * i + e] = s[e];
+    }
+  }
 }
 
 // ----------------------------------------------------------------------------
