@@ -258,12 +258,13 @@ dv_status dv_paged_append(const dv_paged_kv* kv, const float* k, const float* v,
   a.status = static_cast<int*>(ws);
   a.h = kv->h_kv;
   a.dh8 = kv->dh / 8;
-  a.chunks = (long long)T * a.h * a.dh8;
+  const long long chunks = (long long)T * a.h * a.dh8;
+  if (chunks > INT32_MAX - PA_THREADS) return DV_ERR_UNSUPPORTED;
+  a.chunks = (int)chunks;
   a.page = kv->page;
   a.stride_rows = (int)stride_rows(kv);
   a.n_slots = kv->n_pages * kv->page;
-  const long long grid = (a.chunks + PA_THREADS - 1) / PA_THREADS;
-  if (grid > INT32_MAX) return DV_ERR_UNSUPPORTED;
+  const int grid = (a.chunks + PA_THREADS - 1) / PA_THREADS;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return cuda_status(kv->kvdtype == DV_BF16
                          ? launch(paged_append_kernel<bf16>, dim3((unsigned)grid), dim3(PA_THREADS), 0, st, a)

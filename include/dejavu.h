@@ -484,7 +484,7 @@ DV_API dv_status dv_page_tables(const int32_t* want, int R, int page, int n_page
  * the pools' dtype, into slots[t] (device int32). A negative slot is passed
  * over (padding); one outside the pools is passed over and flagged
  * (DV_DEV_INDEX_RANGE). Two tokens must not have the same slot (which of them
- * is kept is not defined). */
+ * is kept is not defined). T * h_kv * dh / 8 must be below 2^31. */
 DV_API dv_status dv_paged_append(const dv_paged_kv* kv, const float* k, const float* v, int T, const int32_t* slots,
                                  void* ws, size_t ws_bytes, dv_stream_t stream);
 
