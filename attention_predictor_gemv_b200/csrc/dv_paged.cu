@@ -1,5 +1,7 @@
 // Paged key-value cache: argument checks, launches and C entry points.
 // Declarations and argument contracts: include/dejavu.h.
+#include <algorithm>
+
 #include "dv_paged.cuh"
 #include "dv_paged_proj.cuh"
 #include "dv_launch.cuh"
@@ -26,7 +28,9 @@ cudaError_t launch_attn(PagedAttnArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long cap = (long long)a.W * a.page;
   const long long most = a.B * ((cap + UNIT - 1) / UNIT) * (long long)a.rows * a.NQ;  // units, at most
-  const long long want = (most + Shape::WARPS - 1) / Shape::WARPS, have = (long long)sm_count() * per_sm;
+  // a unit for each warp, and a CTA for each item where there are few
+  const long long items = std::min((long long)a.B * a.rows * a.NQ, most);
+  const long long want = std::max((most + Shape::WARPS - 1) / Shape::WARPS, items), have = (long long)sm_count() * per_sm;
   return launch_main(paged_attn_kernel<KT, NB, QR>, dim3((unsigned)(want < 1 ? 1 : want < have ? want : have)),
                      dim3(32 * Shape::WARPS), smem, st, a);
 }
