@@ -222,7 +222,7 @@ dv_status dv_page_tables(const int32_t* want, int R, int page, int n_pages, int 
                         (const void*)slots, (const void*)offsets, (const void*)granted})
     if (!ok_opt(p)) return DV_ERR_ALIGN;
   // tokens, slots and pages of all requests are counted with 31 bits
-  if (R > PAGED_MAX_ROWS || page > INT32_MAX / n_pages || page > INT32_MAX / R / W || max_tokens > INT32_MAX - 4)
+  if (R > PAGED_MAX_ROWS || page > INT32_MAX / n_pages || page > INT32_MAX / 2 / R / W || max_tokens > INT32_MAX - 4)
     return DV_ERR_UNSUPPORTED;
   const dv_status s = ws_check(ws, ws_bytes, WS_HEADER);
   if (s != DV_OK) return s;
@@ -286,7 +286,7 @@ dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, c
   for (const void* p : {(const void*)q, (const void*)table, (const void*)lens, (const void*)head_idx,
                         (const void*)head_count, (const void*)out, (const void*)lse})
     if (!ok_opt(p)) return DV_ERR_ALIGN;
-  if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - 32) / W) return DV_ERR_UNSUPPORTED;
+  if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - 32) / W || h_q > INT32_MAX / kv->dh) return DV_ERR_UNSUPPORTED;
   const int rows = head_idx ? kh_max : kv->h_kv, G = h_q / kv->h_kv;
   // the units of all requests and heads are numbered with 31 bits
   if (((long long)W * kv->page + 16) / 16 * B * ((G + 7) / 8) > INT32_MAX / (rows > 0 ? rows : 1)) return DV_ERR_UNSUPPORTED;

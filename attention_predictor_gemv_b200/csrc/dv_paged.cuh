@@ -401,28 +401,39 @@ __global__ void __launch_bounds__(PA_THREADS) paged_token_kernel(PagedTokenArgs 
 //   out = sum_s p_s V_s / sum_s p_s,  p_s = exp(scale q . K_s),
 // one pass over K and V with a running maximum and sum (base 2).
 //
-// Work: the keys of a (request, head, group of 8 NT query heads) are cut into
-// units of 16 keys, all units form one line, and every warp takes an equal
-// stretch of it, so ragged lengths, few requests and few heads balance alike.
-// A stretch's items that lie inside one warp are finished there; what crosses
+// Work: the keys of an item (request, key-value head, up to 16 query heads) are
+// cut into units of 16 or 32 keys, all units form one line, and every warp
+// takes an equal stretch of it, so ragged lengths, few requests and few heads
+// balance alike. An item inside one stretch is finished there; what crosses
 // warps is joined through shared memory, what crosses CTAs through partials in
-// the workspace, by the last CTA of the item to arrive, in CTA order.
+// the workspace, by the last CTA of the item to arrive, in CTA order: results
+// do not depend on timing.
 //
-// Arithmetic: the products run on mma.sync m16n8k16 (bf16 in, fp32 out) with
-// the keys (then V's channels) as the 16 rows and 8 query heads as the columns.
-// q and p are fp32: they enter as three bf16 terms whose sum is the fp32 value
-// to 2^-25, so only K and V (bf16 by storage) are ever rounded; fp32 caches are
-// split the same way and the six products down to 2^-24 are kept. The tensor
-// core truncates its sums, so chains are kept short and added in fp32 outside.
-// tcgen05 would need 128 rows of A for at most 16 queries and the operands in
-// shared memory; the kernel is bound by HBM either way.
+// Arithmetic: mma.sync m16n8k16 (bf16 in, fp32 out) with the queries as rows,
+// the keys (then V's channels) as columns. q and p are fp32: they enter as
+// three bf16 terms whose sum is the fp32 value to 2^-25, in rows of one
+// fragment where 16 rows have room for them, so of bf16 caches nothing is
+// rounded; fp32 caches are split the same way and the products down to 2^-24
+// are kept. The tensor core truncates its sums, so chains are kept to one unit
+// and added in fp32 outside. The scores' fragment is the second product's
+// operand as it stands. tcgen05 would need 128 rows of A for at most 16 queries.
 //
-// K and V go straight from global memory into the fragments: a lane's 16-byte
-// load of a K row is the k-slots (2t, 2t+1, 2t+8, 2t+9) of two MMAs, with the
-// query's channels permuted alike, and V's channels are spread over the MMA's
-// rows so that one byte permute pairs two keys. So there is no shared-memory
-// staging and no barrier in the loop; the next unit's K is requested once the
-// scores of this one are formed, its V once this one's is used.
+// Data: K and V rows come by 16-byte asynchronous copies, whole rows side by
+// side, into the warp's own two slots (pitch one piece over the row, so the
+// fragments' 16-byte reads have no bank conflicts); K of the next unit is
+// requested once the scores of this one are formed, its V once this one's is
+// used, the next item's q with it. No barrier in the loop. Any page size and
+// alignment of pages costs the same (54.5 us with pages of 16, 55.0 with 8).
+// Measured on the way: fragments loaded from global memory directly 71 us
+// (8 rows of 64 bytes a load hold the L1 path at 4.8 TB/s), row-wise bulk copies
+// 4.3 TB/s in a copy test that ran 6.3 TB/s with these; 4 warps in two CTAs the
+// same; three CTAs' worth of shorter stretches per SM slower (66 us).
+//
+// Bound by HBM for long contexts: 16 requests of 32 heads, 0 to 2176 keys,
+// 54.5 us (5.2 TB/s, 0.80 of the copy bandwidth); 64 requests of 64 heads over
+// 8, 0 to 8192 keys, 190 us (5.7 TB/s, 0.86); one of 131071 keys 98 us (0.83).
+// About 8 us of each are launch, schedule, the first rows' latency and the
+// joins; SMs finish up to 15 % apart. One request of 65 keys: 6.6 us.
 // ----------------------------------------------------------------------------
 constexpr int PGA_JOIN = 16;  // CTAs' partials that one CTA adds, at most (of more, groups first)
 
@@ -573,7 +584,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
   // items, or each item has whole CTAs, where that takes (nearly) as few units a warp; else CTAs share evenly.
   int CE = min((int)gridDim.x, (U + WARPS - 1) / WARPS);  // CTAs with work
   int group = U, ctas = CE;                               // `ctas` CTAs share each `group` units
-  if (same > 0) {
+  if (same > 0 && U > 0) {
     const int items = a.B * IR;
     if (same <= WARPS) {
       const int per = WARPS / same, need = (items + per - 1) / per;
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
 
   const uint32_t row0 = g == 0 ? ~0u : 0u, row1 = g == 1 ? ~0u : 0u;  // (masks: choices by row became branches)
   float o[NB][8][QH][2], m[QH], l[QH];  // (l: this lane's keys)
-  uint32_t qa[NK][4], ql[ONE ? 1 : NK][2], qw[WIDE ? NK : 1][4];  // (WIDE: high, -, middle; low in ql and qx)
+  uint32_t qa[NK][4], ql[ONE ? 1 : NK][2], qw[WIDE ? NK : 1][4];  // (WIDE: high in qa, middle in qw, low in ql and qx)
   uint32_t qx[WIDE ? NK : 1][2];
   float* raw_mine = part_of(warp) + PARTF;
   // q of an item on its way to shared memory

@@ -31,7 +31,7 @@ template <bool ONE>
 __device__ __forceinline__ void a_words(float x, float y, int g, uint32_t& a_top, uint32_t& a_low, uint32_t& b_low) {
   uint32_t h, m, l;
   split3(x, y, h, m, l);
-  // (masks, not choices: a choice by row became branches, a warp's way through each of them)
+  // (masks, not choices: those became branches, and the q, k, v kernel took 60 us for 36)
   const uint32_t row0 = g == 0 ? ~0u : 0u, row1 = g == 1 ? ~0u : 0u;
   a_top = ONE ? (h & row0) | (l & row1) : h;
   a_low = ONE ? m & row0 : m;
@@ -43,10 +43,14 @@ __device__ __forceinline__ void a_words(float x, float y, int g, uint32_t& a_top
 // `all`, k and v of the others) form tiles of 8 rows; a CTA takes an equal
 // share of the tiles, up to four at a time, its warps a share of the d channels
 // each, 128 channels a ring slot. y lies in shared memory, a segment of the
-// channels at a time where it is larger than 64 KB: loaded from L2 within the
-// loop it queued behind the weights in flight (60 us against 26 us at 5376 rows
-// of 12288 channels). k and v are rounded into slots[b]; without
-// `all` the places of the other heads are cleared.
+// channels at a time where it is larger than 64 KB, since loads of it within the
+// loop queue behind the weights in flight. k and v are rounded into slots[b];
+// without `all` the places of the other heads are cleared.
+// 5376 rows of 12288 channels (132 MB), one request: 36 us, 3.7 TB/s; 7680 rows
+// of 4096 channels (63 MB), four requests: 20 us. Bound by the loop's
+// instructions (the terms of y, once per slot) where a CTA has few tiles, and
+// by 4 us before the first rows arrive. Slots of 64 channels of eight tiles took
+// the same time.
 // ----------------------------------------------------------------------------
 constexpr int PQ_TILES = 4, PQ_SLOTS = 2, PQ_PITCH = 256 + 16;
 constexpr int PQ_SLOT = PQ_TILES * 8 * PQ_PITCH;
@@ -161,30 +165,49 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
     const int passes = (t1 - t0 + PQ_TILES - 1) / PQ_TILES, nt = (t1 - t0 + passes - 1) / passes;
     const int blocks = (a.d + 127) >> 7;
     const int nk = (blocks + PP_WARPS - 1 - warp) / PP_WARPS;  // blocks warp, warp + 8, ...: side by side in a row
-    const int units = passes * nk;
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring) + warp * PQ_SLOTS * PQ_SLOT + (lane >> 4) * PQ_PITCH + (lane & 15) * 16;
     const char* mine = ring + warp * PQ_SLOTS * PQ_SLOT;
-    auto request = [&](int u) {
-      if (u < units) {
-        const int pass = u / nk, k = warp + (u - pass * nk) * PP_WARPS;
-        const int ch = k * 128 + (lane & 15) * 8;
-        const uint32_t to = at + (u % PQ_SLOTS) * PQ_SLOT;
+    // what is requested next: pass rp, the warp's block rk; its tiles' rows (this lane's first) and which there are
+    int rp = 0, rk = 0, rs = 0;
+    const char* src[PQ_TILES];
+    unsigned there = 0;
+    auto rows_of_pass = [&]() {
+      there = 0;
+#pragma unroll
+      for (int i = 0; i < PQ_TILES; ++i) {
+        const int t = t0 + rp * nt + i, row = i < nt && t < t1 ? s_row[t - t0] : -1;
+        there |= row >= 0 ? 1u << i : 0u;
+        src[i] = reinterpret_cast<const char*>(a.W + (row >= 0 ? (size_t)(row + (lane >> 4)) * a.d : 0));
+      }
+    };
+    if (nk > 0) rows_of_pass();
+    const size_t two_rows = 4ull * a.d;  // bytes
+    auto request = [&]() {
+      if (nk > 0 && rp < passes) {
+        const int ch = (warp + rk * PP_WARPS) * 128 + (lane & 15) * 8;
+        const uint32_t to = at + rs * PQ_SLOT;
 #pragma unroll
         for (int i = 0; i < PQ_TILES; ++i) {
-          const int t = t0 + pass * nt + i;
-          if (i < nt && t < t1) {
-            const int row = s_row[t - t0];
-            const bool on = row >= 0 && ch < a.d;
-            const __nv_bfloat16* src = a.W + (on ? (size_t)(row + (lane >> 4)) * a.d + ch : 0);
+          if (i >= nt) break;
+          const bool on = (there >> i & 1) && ch < a.d;
+          const char* p = src[i] + (on ? 2 * ch : 0);
 #pragma unroll
-            for (int r = 0; r < 8; r += 2) copy16_or_zero(to + (8 * i + r) * PQ_PITCH, src + (on ? (size_t)r * a.d : 0), on);
+          for (int r = 0; r < 8; r += 2) {
+            copy16_or_zero(to + (8 * i + r) * PQ_PITCH, p, on);
+            if (on) p += two_rows;
           }
+        }
+        rs = rs + 1 == PQ_SLOTS ? 0 : rs + 1;
+        if (++rk == nk) {
+          rk = 0;
+          if (++rp < passes) rows_of_pass();
         }
       }
       copies_commit();
     };
 #pragma unroll
-    for (int u = 0; u < PQ_SLOTS - 1; ++u) request(u);
+    for (int u = 0; u < PQ_SLOTS - 1; ++u) request();
+    int slot = 0;
     for (int pass = 0; pass < passes; ++pass) {
       float acc[PQ_TILES][2] = {};
       for (int i0 = 0; i0 * PQ_STRIDE < a.d; i0 += seg) {
@@ -199,8 +222,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
         }
 #pragma unroll 1
       for (int k = i0; k < min(nk, i0 + seg); ++k) {
-        const int u = pass * nk + k;
-        request(u + PQ_SLOTS - 1);
+        request();
         uint32_t fa[8][4], fb[8][2];
         const float* yp = s_y + (ONE ? 0 : g) * pitch + (k - i0) * PQ_STRIDE + warp * 128 + 16 * t4;
 #pragma unroll
@@ -211,7 +233,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
           a_words<ONE>(x.z, x.w, g, fa[s][2], fa[s][3], fb[s][1]);
         }
         copies_wait<PQ_SLOTS - 1>();
-        const char* w = mine + (u % PQ_SLOTS) * PQ_SLOT + g * PQ_PITCH + t4 * 32;
+        const char* w = mine + slot * PQ_SLOT + g * PQ_PITCH + t4 * 32;
+        slot = slot + 1 == PQ_SLOTS ? 0 : slot + 1;
         float c[PQ_TILES][4];
 #pragma unroll
         for (int piece = 0; piece < 4; ++piece) {
@@ -301,7 +324,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
 // the selected heads. A CTA takes 8 NC columns and all rows, its warps a share
 // of the rows each, 32 rows a ring slot; the weights are the MMA's columns,
 // read by transposing matrix loads. The ring is filled before the wait for the
-// attention, which writes H alone.
+// attention, which writes H alone. 1792 rows of 12288 columns (44 MB), one
+// request: 12 us; 2560 rows of 4096, four requests: 10.5 us; bound by the ring's
+// start and the last round of a ring that is as long as the work.
 // ----------------------------------------------------------------------------
 struct PagedWoArgs {
   const __nv_bfloat16* W;

@@ -474,7 +474,8 @@ typedef struct {
  * free_count_out may be free_count (other arrays must not overlap); kept
  * apart, a repeated call gives the same result again.
  * A length outside [0, W * page] is kept, refused and flagged (DV_DEV_INDEX_RANGE);
- * a free count outside [0, n_pages] is clamped and flagged. */
+ * a free count outside [0, n_pages] is clamped and flagged. n_pages * page must
+ * be below 2^31 and R * W * page below 2^30 (DV_ERR_UNSUPPORTED). */
 DV_API dv_status dv_page_tables(const int32_t* want, int R, int page, int n_pages, int W, const int32_t* lens,
                                 int32_t* lens_out, int32_t* table, int32_t* free_list, const int32_t* free_count,
                                 int32_t* free_count_out, int max_tokens, int32_t* slots, int32_t* offsets,

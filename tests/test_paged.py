@@ -28,11 +28,12 @@ def test_workspace_sizes():
     n = bd.dv_workspace_size(bd.DV_OP_PAGE_TABLES, bd.dims())
     assert n == bd.dv_workspace_size(bd.DV_OP_PAGED_APPEND, bd.dims()) > 0
     a = bd.dv_workspace_size(bd.DV_OP_PAGED_ATTN, bd.dims(dh=64))
-    assert n < a < bd.dv_workspace_size(bd.DV_OP_PAGED_ATTN, bd.dims(dh=128))
+    assert n < a and n < bd.dv_workspace_size(bd.DV_OP_PAGED_ATTN, bd.dims(dh=128))
     for dh in (0, 4, 12, 264):
         assert bd.dv_workspace_size(bd.DV_OP_PAGED_ATTN, bd.dims(dh=dh)) == 0
     m = bd.dv_workspace_size(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=4, d=512, h=8, dh=64, kh_max=8))
     assert m > bd.dv_workspace_size(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=1, d=512, h=8, dh=64, kh_max=2)) > a
+    assert bd.dv_workspace_size(bd.DV_OP_PAGED_ATTN, bd.dims(dh=256)) > bd.dv_workspace_size(bd.DV_OP_PAGED_ATTN, bd.dims(dh=128))
     assert bd.dv_workspace_size(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=17, d=512, h=8, dh=64, kh_max=8)) == 0
     assert bd.dv_workspace_size(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=1, d=512, h=8, dh=96, kh_max=8)) == 0
 
@@ -84,6 +85,8 @@ def test_attn_checks():
         assert _attn(**kw) == bd.DV_ERR_ALIGN, kw
     assert _attn(B=4097) == bd.DV_ERR_UNSUPPORTED
     assert _attn(W=2 ** 27) == bd.DV_ERR_UNSUPPORTED  # W * page
+    assert _attn(h_q=2 ** 26) == bd.DV_ERR_UNSUPPORTED  # h_q * dh
+    assert _attn(B=4096, W=2 ** 21) == bd.DV_ERR_UNSUPPORTED  # units of 16 keys of all requests and heads
     assert _attn(wsb=1 << 16) == bd.DV_ERR_WORKSPACE
     assert _attn(idx=A, cnt=A, kh=0) == bd.DV_OK  # no head: nothing to launch
 
@@ -102,7 +105,7 @@ def test_page_tables_checks():
         assert _tables(**{n: A + 4}) == bd.DV_ERR_ALIGN, n
     for kw in (dict(R=0), dict(page=0), dict(n_pages=0), dict(W=0), dict(max_tokens=-1)):
         assert _tables(**kw) == bd.DV_ERR_ARG, kw
-    for kw in (dict(R=4097), dict(page=2 ** 26), dict(W=2 ** 30), dict(n_pages=2 ** 28)):
+    for kw in (dict(R=4097), dict(page=2 ** 26), dict(W=2 ** 30), dict(n_pages=2 ** 28), dict(R=1, W=1, n_pages=1, page=2 ** 30)):
         assert _tables(**kw) == bd.DV_ERR_UNSUPPORTED, kw
     assert _tables(wsb=16) == bd.DV_ERR_WORKSPACE
 
