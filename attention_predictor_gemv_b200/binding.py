@@ -481,13 +481,21 @@ def _arg(t: Optional[torch.Tensor], dtype, shape, index: int, name: str) -> Opti
     return t.data_ptr()
 
 
+def _ints(t: torch.Tensor, n: int, index: int, name: str) -> int:
+    """Pointer of n contiguous int32 on CUDA device `index`."""
+    if t.dtype is not torch.int32 or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}; expected {n} "
+                         f"torch.int32 on cuda:{index}, contiguous")
+    return t.data_ptr()
+
+
 def _ws_arg(ws: torch.Tensor, index: int) -> int:
     if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"ws: {ws.dtype} on {ws.device}; expected a workspace on cuda:{index}")
     return ws.data_ptr()
 
 
-_i32, _f32 = torch.int32, torch.float32
+_f32 = torch.float32
 
 
 def _launch(fn, name: str, index: int, stream, *args):
@@ -513,15 +521,14 @@ def dv_page_tables(want, lens, lens_out, table, free_list, free_count, free_coun
                    stream=None):
     """Block tables [R][W], slots and the free stack from the requests'
     current and wanted lengths (int32, on the device)."""
-    dev, i32 = want.get_device(), _i32
+    dev = want.get_device()
     R, W = table.shape
-    n_pages, max_tokens = free_list.shape[0], slots.shape[0]
-    _launch(_lib_dv_page_tables, "dv_page_tables", dev, stream, _arg(want, i32, (R,), dev, "want"), R, int(page), n_pages, W,
-            _arg(lens, i32, (R,), dev, "lens"), _arg(lens_out, i32, (R,), dev, "lens_out"),
-            _arg(table, i32, (R, W), dev, "table"), _arg(free_list, i32, (n_pages,), dev, "free_list"),
-            _arg(free_count, i32, (1,), dev, "free_count"), _arg(free_count_out, i32, (1,), dev, "free_count_out"),
-            max_tokens, _arg(slots, i32, (max_tokens,), dev, "slots"), _arg(offsets, i32, (R + 1,), dev, "offsets"),
-            _arg(granted, i32, (R,), dev, "granted"), _ws_arg(ws, dev), ws.numel())
+    n_pages, max_tokens = free_list.numel(), slots.numel()
+    _launch(_lib_dv_page_tables, "dv_page_tables", dev, stream, _ints(want, R, dev, "want"), R, int(page), n_pages, W,
+            _ints(lens, R, dev, "lens"), _ints(lens_out, R, dev, "lens_out"), _ints(table, R * W, dev, "table"),
+            _ints(free_list, n_pages, dev, "free_list"), _ints(free_count, 1, dev, "free_count"),
+            _ints(free_count_out, 1, dev, "free_count_out"), max_tokens, _ints(slots, max_tokens, dev, "slots"),
+            _ints(offsets, R + 1, dev, "offsets"), _ints(granted, R, dev, "granted"), _ws_arg(ws, dev), ws.numel())
 
 
 def dv_paged_append(kv: PagedKV, k, v, slots, ws, stream=None):
@@ -531,7 +538,7 @@ def dv_paged_append(kv: PagedKV, k, v, slots, ws, stream=None):
     if T == 0:
         return
     _launch(_lib_dv_paged_append, "dv_paged_append", dev, stream, kv.ref, _arg(k, _f32, shape, dev, "k"),
-            _arg(v, _f32, shape, dev, "v"), T, _arg(slots, _i32, (T,), dev, "slots"), _ws_arg(ws, dev),
+            _arg(v, _f32, shape, dev, "v"), T, _ints(slots, T, dev, "slots"), _ws_arg(ws, dev),
             ws.numel())
 
 
@@ -540,23 +547,23 @@ def dv_paged_attn(q, kv: PagedKV, table, lens, scale, out, ws, lse=None, head_id
     [B][h_q][dh]; with a set head_idx / head_count of key-value heads they are
     [B][kh_max * G][dh], G query heads for each place of the set, kh_max =
     len(head_idx), and h_q = G * h_kv."""
-    dev, i32, f32 = kv.index, _i32, _f32
+    dev, f32 = kv.index, _f32
     B, rows, dh = q.shape
     heads = kv.h_kv if head_idx is None else head_idx.shape[0]
     if head_idx is not None and head_count is None or heads == 0 or rows % heads != 0 or dh != kv.dh:
         raise ValueError(f"q: {tuple(q.shape)} for {heads} key-value heads of {kv.dh} channels")
     W = table.shape[1]
     _launch(_lib_dv_paged_attn, "dv_paged_attn", dev, stream, kv.ref, _arg(q, f32, (B, rows, dh), dev, "q"), B,
-            rows // heads * kv.h_kv, _arg(table, i32, (B, W), dev, "table"), W, _arg(lens, i32, (B,), dev, "lens"),
-            float(scale), _arg(head_idx, i32, (heads,), dev, "head_idx"), _arg(head_count, i32, (1,), dev, "head_count"),
-            heads if head_idx is not None else 0, _arg(out, f32, (B, rows, dh), dev, "out"),
+            rows // heads * kv.h_kv, _ints(table, B * W, dev, "table"), W, _ints(lens, B, dev, "lens"),
+            float(scale), None if head_idx is None else _ints(head_idx, heads, dev, "head_idx"),
+            None if head_count is None else _ints(head_count, 1, dev, "head_count"), heads if head_idx is not None else 0, _arg(out, f32, (B, rows, dh), dev, "out"),
             _arg(lse, f32, (B, rows), dev, "lse"), _ws_arg(ws, dev), ws.numel())
 
 
 def dv_sparse_mha_paged(y, Wqkv, bqkv, WOt, bO, kv: PagedKV, table, lens, slots, scale, head_idx, head_count, kh_max, out,
                         ws, accumulate=False, exact_kv=False, stream=None):
     """dv_sparse_mha over a paged cache: per-row lengths [B], the new token's slot [B]."""
-    dev, i32, f32 = kv.index, _i32, _f32
+    dev, f32 = kv.index, _f32
     B, d = y.shape
     h, dh, W = kv.h_kv, kv.dh, table.shape[1]
     if head_idx.shape[0] < kh_max:
@@ -564,7 +571,6 @@ def dv_sparse_mha_paged(y, Wqkv, bqkv, WOt, bO, kv: PagedKV, table, lens, slots,
     _launch(_lib_dv_sparse_mha_paged, "dv_sparse_mha_paged", dev, stream, _arg(y, f32, (B, d), dev, "y"), B, d,
             _arg(Wqkv, Wqkv.dtype, (h, 3, dh, d), dev, "Wqkv"), _arg(bqkv, f32, (h, 3, dh), dev, "bqkv"),
             _arg(WOt, Wqkv.dtype, (h, dh, d), dev, "WOt"), _arg(bO, f32, (d,), dev, "bO"), _wdt(Wqkv), kv.ref,
-            _arg(table, i32, (B, W), dev, "table"), W, _arg(lens, i32, (B,), dev, "lens"),
-            _arg(slots, i32, (B,), dev, "slots"), float(scale), _arg(head_idx, i32, tuple(head_idx.shape), dev, "head_idx"),
-            _arg(head_count, i32, (1,), dev, "head_count"), int(kh_max), _arg(out, f32, (B, d), dev, "out"),
+            _ints(table, B * W, dev, "table"), W, _ints(lens, B, dev, "lens"), _ints(slots, B, dev, "slots"), float(scale),
+            _ints(head_idx, head_idx.numel(), dev, "head_idx"), _ints(head_count, 1, dev, "head_count"), int(kh_max), _arg(out, f32, (B, d), dev, "out"),
             int(bool(accumulate)), int(bool(exact_kv)), _ws_arg(ws, dev), ws.numel())

@@ -444,6 +444,50 @@ def test_sparse_mha_paged_matches_the_model(wdt, B, dh, heads, exact, acc, bias)
                 assert np.all(np.abs(got_row - want_row) <= np.abs(want_row) * 2.0 ** -7 + scale * 2.0 ** -12)
 
 
+@pytest.mark.parametrize("B, d, h, heads, exact", [
+    (7, 5000, 32, list(range(32)), False),  # channels in segments, weight tiles in several passes, odd blocks
+    (2, 20480, 3, [0, 2], True),            # more column blocks of W^O than SMs
+    (1, 12296, 40, list(range(0, 40, 2)), False), (3, 264, 8, [7], True), (8, 1032, 5, [0, 1, 2, 3, 4], False)])
+def test_sparse_mha_paged_at_sizes_that_do_not_divide(B, d, h, heads, exact):
+    dh, page = 64, 12
+    g = gen(d)
+    W = (torch.randn(h, 3, dh, d, generator=g, device="cuda") * d ** -0.5).to(BF16)
+    WOt = (torch.randn(h, dh, d, generator=g, device="cuda") * d ** -0.5).to(BF16)
+    bqkv = 0.3 * torch.randn(h, 3, dh, generator=g, device="cuda")
+    lens = [(29 * (b + 1)) % 60 + 1 for b in range(B)]
+    K, V, table, lens_t = make_cache(lens, h, dh, page, BF16, B)
+    slots = [int(table[b, (n - 1) // page]) * page + (n - 1) % page for b, n in enumerate(lens)]
+    y = torch.randn(B, d, generator=g, device="cuda")
+    out = torch.full((B, d), 7.0, device="cuda")
+    Kf, Vf = torch.nan_to_num(K.double()), torch.nan_to_num(V.double())
+    qkv = torch.einsum("bd,hmcd->bhmc", y.double(), W.double()) + bqkv.double()
+    ws = bd.workspace(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=B, d=d, h=h, dh=dh, kh_max=len(heads)))
+    bd.dv_sparse_mha_paged(y, W, bqkv, WOt, None, bd.PagedKV(K, V), table, lens_t, i32(slots), 0.125, i32(heads), i32([len(heads)]),
+                           len(heads), out, ws, exact_kv=exact)
+    torch.cuda.synchronize()
+    assert bd.dv_read_device_status(ws) == 0
+    want = torch.zeros(B, d, dtype=torch.float64, device="cuda")
+    for b, sl in enumerate(slots):
+        p, o = divmod(sl, page)
+        Kf[p, :, o], Vf[p, :, o] = 0, 0
+        for i in range(h) if exact else heads:
+            # a stored value is the product's, rounded once: half a step of bf16, and the fp32 sum's error of 2^-18 of its terms
+            for pool, dst, m in ((K, Kf, 1), (V, Vf, 2)):
+                ref = qkv[b, i, m]
+                mag = (y[b].double().abs() * W[i, m].double().abs()).sum(1) + bqkv[i, m].double().abs()
+                assert ((pool[p, i, o].double() - ref).abs() <= ref.abs() * 2.0 ** -8 + mag * 2.0 ** -18).all()
+                dst[p, i, o] = pool[p, i, o].double()  # (the attention reads what the pages hold)
+        if not exact:
+            for i in set(range(h)) - set(heads):
+                assert not K[p, i, o].any() and not V[p, i, o].any()
+        for i in heads:
+            pages = table[b, : -(-lens[b] // page)].long()
+            k, v = (t[pages, i].reshape(-1, dh)[: lens[b]] for t in (Kf, Vf))
+            want[b] += (torch.softmax((k @ qkv[b, i, 0]) * 0.125, 0) @ v) @ WOt[i].double()
+    # 64 len(heads) terms a sum, each of fp32 operands in three bf16 terms: far inside 2^-16 of the result's norm
+    assert (out.double() - want).norm() <= 2.0 ** -16 * want.norm()
+
+
 def test_paged_block_equals_the_contiguous_one():
     """Equal lengths, the same values: dv_sparse_mha_paged against dv_sparse_mha."""
     B, d, h, dh, page, L = 2, 1024, 8, 128, 16, 100
