@@ -154,10 +154,12 @@ cudaError_t run_paged_qkv(const dv_paged_kv* kv, const void* W, const float* bia
   a.page = kv->page;
   a.stride_rows = (int)stride_rows(kv);
   a.n_slots = kv->n_pages * kv->page;
-  auto kern = B == 1 ? paged_qkv_kernel<1> : paged_qkv_kernel<8>;
-  cudaError_t e = allow_smem(kern, paged_qkv_smem());
+  const bool one = B == 1 && d <= PT_MAX_D;
+  auto kern = one ? paged_qkv_one_kernel : paged_qkv_kernel;
+  const size_t smem = one ? paged_qkv_one_smem() : paged_qkv_smem();
+  cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_main(kern, dim3(sm_count()), dim3(PP_THREADS), paged_qkv_smem(), st, a);
+  return launch_main(kern, dim3(sm_count()), dim3(PP_THREADS), smem, st, a);
 }
 
 namespace {

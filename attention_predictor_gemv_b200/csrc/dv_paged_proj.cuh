@@ -41,24 +41,15 @@ __device__ __forceinline__ void a_words(float x, float y, int g, uint32_t& a_top
 // ----------------------------------------------------------------------------
 // q, k, v. Weight rows Wqkv[head][3][dh][d] of the selected heads (and, with
 // `all`, k and v of the others) form tiles of 8 rows; a CTA takes an equal
-// share of the tiles, up to four at a time, its warps a share of the d channels
-// each, 128 channels a ring slot. y lies in shared memory, a segment of the
-// channels at a time where it is larger than 64 KB, since loads of it within the
-// loop queue behind the weights in flight. k and v are rounded into slots[b];
-// without `all` the places of the other heads are cleared.
-// 5376 rows of 12288 channels (132 MB), one request: 36 us, 3.7 TB/s; 7680 rows
-// of 4096 channels (63 MB), four requests: 20 us. Bound by the loop's
-// instructions (the terms of y, once per slot) where a CTA has few tiles, and
-// by 4 us before the first rows arrive. Slots of 64 channels of eight tiles took
-// the same time.
+// share of the tiles, its warps a share of the d channels each. y lies in shared
+// memory, since loads of it within the loop queue behind the weights in flight.
+// k and v are rounded into slots[b]; without `all` the places of the other heads
+// are cleared. Two forms, below.
+// 5376 rows of 12288 channels (132 MB), one request: 31 us under a profiler,
+// 4.3 TB/s; 7680 rows of 4096 channels (63 MB), four requests: 20 us. Bound by
+// the 4 us before the first rows arrive, by CTAs of five tiles where the mean is
+// 4.5, and with more requests by the loop's instructions.
 // ----------------------------------------------------------------------------
-constexpr int PQ_TILES = 4, PQ_SLOTS = 2, PQ_PITCH = 256 + 16;
-constexpr int PQ_SLOT = PQ_TILES * 8 * PQ_PITCH;
-constexpr int PQ_STRIDE = 128 * PP_WARPS;                // channels that the warps take side by side
-constexpr int PQ_YF = 16384;                             // floats of y at a time
-constexpr int PQ_YPAD = 4;                               // of each request's row, in floats
-constexpr int PQ_MAX_TILES = 512;  // of a CTA: 3 * 1024 heads * 16 tiles over 100 SMs or more
-
 struct PagedQkvArgs {
   const __nv_bfloat16* W;
   const float* bias;
@@ -71,16 +62,243 @@ struct PagedQkvArgs {
   int B, d, h, dh, kh_max, all, page, stride_rows, n_slots;
 };
 
+// A tile's place: its head (-1: none), which of q, k, v, first channel, place in the set
+struct QkvTile {
+  int head, m, c, j;
+};
+
+// The set's size, clamped and flagged, and the heads outside it in order (s_rest, s_nrest); by a whole block, first of
+// all: with the first weights on their way it took 6 us more at four requests.
+__device__ __forceinline__ int qkv_lists(const PagedQkvArgs& a, short* s_rest, int* s_nrest) {
+  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31;
+  int nsel = *a.head_count;
+  if (nsel < 0 || nsel > a.kh_max) {
+    if (blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_CLAMPED);
+    nsel = nsel < 0 ? 0 : a.kh_max;
+  }
+  for (int i = tid; i < a.h; i += nth) s_rest[i] = 0;
+  __syncthreads();
+  for (int j = tid; j < nsel; j += nth) {
+    const int head = a.head_idx[j];
+    if (head >= 0 && head < a.h) s_rest[head] = 1;
+    else if (blockIdx.x == 0) raise_status(a.status, ST_RANGE);
+  }
+  __syncthreads();
+  if (tid < 32) {
+    int n = 0;
+    for (int i0 = 0; i0 < a.h; i0 += 32) {
+      const bool rest = i0 + lane < a.h && !s_rest[min(i0 + lane, a.h - 1)];
+      const unsigned in = __ballot_sync(0xffffffffu, rest);
+      __syncwarp();
+      if (rest) s_rest[n + __popc(in & ((1u << lane) - 1u))] = (short)(i0 + lane);  // (never past what was read)
+      __syncwarp();
+      n += __popc(in);
+    }
+    if (lane == 0) *s_nrest = n;
+  }
+  __syncthreads();
+  return nsel;
+}
+
+__device__ __forceinline__ QkvTile qkv_tile(const PagedQkvArgs& a, int nsel, const short* s_rest, int t) {
+  const int per = a.dh >> 3, sel_tiles = nsel * 3 * per;  // tiles of one head's q, k or v; of the set
+  QkvTile p;
+  if (t < sel_tiles) {
+    p.j = t / (3 * per);
+    const int r = t - p.j * 3 * per;
+    p.m = r / per;
+    p.c = (r - p.m * per) * 8;
+    p.head = a.head_idx[p.j];
+    if (p.head >= a.h) p.head = -1;
+  } else {
+    const int u = t - sel_tiles, i = u / (2 * per), r = u - i * 2 * per;
+    p.j = -1;
+    p.m = 1 + r / per;
+    p.c = (r - (p.m - 1) * per) * 8;
+    p.head = s_rest[i];
+  }
+  return p;
+}
+
+// One sum to its place: q to the workspace, k and v, rounded once, to their pages
+__device__ __forceinline__ void qkv_store(const PagedQkvArgs& a, const QkvTile& p, int b, int c, float v) {
+  if (a.bias) v += a.bias[(size_t)(p.head * 3 + p.m) * a.dh + c];
+  if (p.m == 0) {
+    a.q[((size_t)b * a.kh_max + p.j) * a.dh + c] = v;
+    return;
+  }
+  const int slot = a.slots[b];
+  if (slot >= 0 && slot < a.n_slots) {
+    const int pg = slot / a.page;
+    const long long row = (long long)pg * a.stride_rows + p.head * a.page + (slot - pg * a.page);
+    (p.m == 1 ? a.K : a.V)[row * a.dh + c] = __float2bfloat16_rn(v);
+  } else if (slot >= 0) {
+    raise_status(a.status, ST_RANGE);
+  }
+}
+
+// The places of the heads outside the set
+__device__ __forceinline__ void qkv_clear(const PagedQkvArgs& a, const short* s_rest, int n_rest) {
+  const int n = n_rest * a.B, vecs = a.dh >> 3;  // (head, request) pairs, 16-byte vectors of each
+  for (int x = blockIdx.x * blockDim.x + threadIdx.x; x < n * vecs; x += gridDim.x * blockDim.x) {
+    const int pr = x / vecs, v = x - pr * vecs, b = pr % a.B, head = s_rest[pr / a.B];
+    const int slot = a.slots[b];
+    if (slot < 0 || slot >= a.n_slots) {
+      if (slot >= 0) raise_status(a.status, ST_RANGE);
+      continue;
+    }
+    const int pg = slot / a.page;
+    const long long row = (long long)pg * a.stride_rows + head * a.page + (slot - pg * a.page);
+    reinterpret_cast<uint4*>(a.K)[row * vecs + v] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(a.V)[row * vecs + v] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+constexpr int PQ_MAX_TILES = 512;  // of a CTA: 3 * 1024 heads * 16 tiles over 100 SMs or more
+
+// One request: a tile of 8 rows at a time, 512 channels of each row a warp and ring slot, so that what lies together in
+// memory is read together; y's terms, formed once, come from shared memory. For up to 12288 channels: 31 us at the
+// larger size above, where the other form took 34 us.
+constexpr int PT_CW = 512, PT_PITCH = 2 * PT_CW + 16, PT_SLOT = 8 * PT_PITCH, PT_SLOTS = 2, PT_MAX_D = 12288;
+constexpr int PT_HOLD = 8;  // tiles whose sums are kept before the warps' are added
+constexpr int PT_RING = PP_WARPS * PT_SLOTS * PT_SLOT, PT_RED = PT_HOLD * PP_WARPS * 8 * 4;
+constexpr size_t paged_qkv_one_smem() { return PT_RING + PT_RED + 3 * 2 * (PT_MAX_D + 8); }
+static_assert(paged_qkv_one_smem() + 2 * PTK_MAX_H + 4 * PQ_MAX_TILES + 1024 <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_one_kernel(PagedQkvArgs a) {
+  constexpr int CW = PT_CW, SLOTS = PT_SLOTS, PITCH = PT_PITCH, CPR = CW / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(16) char ring[];
+  __shared__ short s_rest[PTK_MAX_H];
+  __shared__ int s_nrest, s_row[PQ_MAX_TILES];  // a tile's first weight row, -1: none
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  float* red = reinterpret_cast<float*>(ring + PP_WARPS * SLOTS * PT_SLOT);  // [tiles held][warps][8 rows]
+  __nv_bfloat16* s_y = reinterpret_cast<__nv_bfloat16*>(ring + PP_WARPS * SLOTS * PT_SLOT + PT_RED);
+  griddep_wait();
+  griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
+  const int nsel = qkv_lists(a, s_rest, &s_nrest);
+  const int tiles = (nsel * 3 + (a.all ? s_nrest * 2 : 0)) * (a.dh >> 3);
+  const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x), t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
+  for (int t = t0 + tid; t < t1; t += PP_THREADS) {
+    const QkvTile p = qkv_tile(a, nsel, s_rest, t);
+    s_row[t - t0] = p.head < 0 ? -1 : (p.head * 3 + p.m) * a.dh + p.c;
+  }
+  __syncthreads();
+  const int blocks = (a.d + CW - 1) / CW, nk = (blocks + PP_WARPS - 1 - warp) / PP_WARPS;  // blocks warp, warp + 8, ...
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * SLOTS * PT_SLOT;
+  int rt = t0, rk = 0, rs = 0;  // requested next: tile, block, slot
+  auto request = [&]() {
+    if (rt < t1 && nk > 0) {
+      const int row = s_row[rt - t0], ch0 = (warp + rk * PP_WARPS) * CW;
+      const uint32_t to = base + rs * PT_SLOT;
+      const __nv_bfloat16* src = a.W + (row >= 0 ? (size_t)row * a.d + ch0 : 0);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+#pragma unroll
+        for (int c = lane; c < CPR; c += 32) {
+          const bool on = row >= 0 && ch0 + 8 * c < a.d;
+          copy16_or_zero(to + r * PITCH + c * 16, src + (on ? 8 * c : 0), on);
+        }
+        if (row >= 0) src += a.d;
+      }
+      rs = rs + 1 == SLOTS ? 0 : rs + 1;
+      if (++rk == nk) rk = 0, ++rt;
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int u = 0; u < SLOTS - 1; ++u) request();
+  // y's terms: high, middle, low [B][pitch]
+  const int width = blocks * CW, pitch = width + 8;
+  for (int c = 4 * tid; c < width; c += 4 * PP_THREADS) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.d) v = *reinterpret_cast<const float4*>(a.y + c);
+    uint2 h, m, l;
+    split3(v.x, v.y, h.x, m.x, l.x);
+    split3(v.z, v.w, h.y, m.y, l.y);
+    *reinterpret_cast<uint2*>(s_y + c) = h;
+    *reinterpret_cast<uint2*>(s_y + pitch + c) = m;
+    *reinterpret_cast<uint2*>(s_y + 2 * pitch + c) = l;
+  }
+  __syncthreads();
+  // row 0's lanes have y's high and middle terms, row 1's the low ones
+  const __nv_bfloat16* y_top = s_y + (g == 1 ? 2 * pitch : 0) + warp * CW + 16 * t4;
+  const __nv_bfloat16* y_mid = s_y + pitch + warp * CW + 16 * t4;
+  const uint32_t on_top = g < 2 ? ~0u : 0u, on_mid = g == 0 ? ~0u : 0u;
+  int slot = 0;
+#pragma unroll 1
+  for (int ta = t0; ta < t1; ta += PT_HOLD) {
+    const int held = min(PT_HOLD, t1 - ta);
+#pragma unroll 1
+    for (int i = 0; i < held; ++i) {
+      float acc[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int k = 0; k < nk; ++k) {
+        request();
+        copies_wait<SLOTS - 1>();
+        const char* w = ring + (warp * SLOTS + slot) * PT_SLOT + g * PITCH + t4 * 32;
+        slot = slot + 1 == SLOTS ? 0 : slot + 1;
+        const int ko = k * PP_WARPS * CW;
+        float c[4][4];
+#pragma unroll
+        for (int p = 0; p < CW / 32; ++p) {  // 16 bytes: eight channels, two steps; four sums side by side
+          const int at = 64 * (p >> 1) + 8 * (p & 1);
+          const uint4 v = *reinterpret_cast<const uint4*>(w + 2 * at);
+          const uint4 h = *reinterpret_cast<const uint4*>(y_top + ko + at), m = *reinterpret_cast<const uint4*>(y_mid + ko + at);
+          const uint32_t f0[4] = {h.x & on_top, m.x & on_mid, h.y & on_top, m.y & on_mid};
+          const uint32_t f1[4] = {h.z & on_top, m.z & on_mid, h.w & on_top, m.w & on_mid};
+          float(&x)[4] = c[2 * (p & 1)], (&z)[4] = c[2 * (p & 1) + 1];
+          if (p < 2) {
+            mma_bf16_first(x, f0, v.x, v.y);
+            mma_bf16_first(z, f1, v.z, v.w);
+          } else {
+            mma_bf16(x, f0, v.x, v.y);
+            mma_bf16(z, f1, v.z, v.w);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          acc[e] += ((c[0][e] + c[0][2 + e]) + (c[1][e] + c[1][2 + e])) + ((c[2][e] + c[2][2 + e]) + (c[3][e] + c[3][2 + e]));
+        __syncwarp();  // the slot is free
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float v = acc[e] + __shfl_xor_sync(0xffffffffu, acc[e], 4);
+        if (g == 0) red[(i * PP_WARPS + warp) * 8 + 2 * t4 + e] = v;
+      }
+    }
+    __syncthreads();
+    if (tid < held * 8) {
+      const int r = tid & 7, i = tid >> 3;
+      const QkvTile p = qkv_tile(a, nsel, s_rest, ta + i);
+      if (p.head >= 0) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < PP_WARPS; ++w) v += red[(i * PP_WARPS + w) * 8 + r];
+        qkv_store(a, p, 0, p.c + r, v);
+      }
+    }
+    __syncthreads();
+  }
+  if (!a.all) qkv_clear(a, s_rest, s_nrest);
+}
+
+// More requests (or channels): they are the rows; a slot holds four tiles of 128 channels, and y's terms are formed once
+// for them, from y in shared memory (a segment of the channels at a time where it is larger than 64 KB). The form above
+// took 25 us for 20 us at four requests; slots of 64 channels of eight tiles, or 16 warps, the same time.
+constexpr int PQ_TILES = 4, PQ_SLOTS = 2, PQ_PITCH = 256 + 16;
+constexpr int PQ_SLOT = PQ_TILES * 8 * PQ_PITCH;
+constexpr int PQ_STRIDE = 128 * PP_WARPS;                // channels that the warps take side by side
+constexpr int PQ_YF = 16384;                             // floats of y at a time
+constexpr int PQ_YPAD = 4;                               // of each request's row, in floats
 constexpr size_t PQ_RING = (size_t)PP_WARPS * PQ_SLOTS * PQ_SLOT;
 constexpr size_t paged_qkv_smem() { return PQ_RING + 4 * (PQ_YF + PP_MAX_B * PQ_YPAD); }
-static_assert(paged_qkv_smem() + 4 * PTK_MAX_H + PP_WARPS * PQ_TILES * 8 * 9 * 4 + 4 * PQ_MAX_TILES + 1024 <= 227 * 1024, "shared memory");
+static_assert(paged_qkv_smem() + 2 * PTK_MAX_H + PP_WARPS * PQ_TILES * 8 * 9 * 4 + 4 * PQ_MAX_TILES + 1024 <= 227 * 1024, "shared memory");
 
-template <int QR>
 __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a) {
-  constexpr bool ONE = QR == 1;
+  constexpr int QR = PP_MAX_B;
   extern __shared__ __align__(16) char ring[];
-  __shared__ short s_head[PTK_MAX_H], s_rest[PTK_MAX_H];
-  __shared__ float red[PP_WARPS][PQ_TILES * 8][QR + (QR > 1)];
+  __shared__ short s_rest[PTK_MAX_H];
+  __shared__ float red[PP_WARPS][PQ_TILES * 8][QR + 1];
   __shared__ int s_nrest, s_row[PQ_MAX_TILES];  // a tile's first weight row, -1: none
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   griddep_wait();
@@ -100,64 +318,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
   };
   request_y(0);
 
-  // selected heads in order, -1 where out of range; the others in order
-  int nsel = *a.head_count;
-  if (nsel < 0 || nsel > a.kh_max) {
-    if (blockIdx.x == 0 && tid == 0) raise_status(a.status, ST_CLAMPED);
-    nsel = nsel < 0 ? 0 : a.kh_max;
-  }
-  for (int i = tid; i < a.h; i += PP_THREADS) s_rest[i] = 0;
-  __syncthreads();
-  for (int j = tid; j < nsel; j += PP_THREADS) {
-    int head = a.head_idx[j];
-    if (head < 0 || head >= a.h) {
-      if (blockIdx.x == 0) raise_status(a.status, ST_RANGE);
-      head = -1;
-    } else {
-      s_rest[head] = 1;
-    }
-    s_head[j] = (short)head;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int n = 0;
-    for (int i0 = 0; i0 < a.h; i0 += 32) {
-      const bool rest = i0 + lane < a.h && !s_rest[min(i0 + lane, a.h - 1)];
-      const unsigned in = __ballot_sync(0xffffffffu, rest);
-      __syncwarp();
-      if (rest) s_rest[n + __popc(in & ((1u << lane) - 1u))] = (short)(i0 + lane);  // (never past what was read)
-      __syncwarp();
-      n += __popc(in);
-    }
-    if (lane == 0) s_nrest = n;
-  }
-  __syncthreads();
-  const int per = a.dh >> 3;  // tiles of one head's q, k or v
-  const int sel_tiles = nsel * 3 * per, tiles = sel_tiles + (a.all ? s_nrest * 2 * per : 0);
+  const int nsel = qkv_lists(a, s_rest, &s_nrest);
+  const int tiles = (nsel * 3 + (a.all ? s_nrest * 2 : 0)) * (a.dh >> 3);
   const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x), t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
-
-  // A tile's place: its head (-1: none), which of q, k, v, first channel, place in the set
-  struct Tile { int head, m, c, j; };
-  auto tile_at = [&](int t) {
-    Tile p;
-    if (t < sel_tiles) {
-      p.j = t / (3 * per);
-      const int r = t - p.j * 3 * per;
-      p.m = r / per;
-      p.c = (r - p.m * per) * 8;
-      p.head = s_head[p.j];
-    } else {
-      const int u = t - sel_tiles, i = u / (2 * per), r = u - i * 2 * per;
-      p.j = -1;
-      p.m = 1 + r / per;
-      p.c = (r - (p.m - 1) * per) * 8;
-      p.head = s_rest[i];
-    }
-    return p;
-  };
-
   for (int t = t0 + tid; t < t1; t += PP_THREADS) {
-    const Tile p = tile_at(t);
+    const QkvTile p = qkv_tile(a, nsel, s_rest, t);
     s_row[t - t0] = p.head < 0 ? -1 : (p.head * 3 + p.m) * a.dh + p.c;
   }
   __syncthreads();
@@ -224,13 +389,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
       for (int k = i0; k < min(nk, i0 + seg); ++k) {
         request();
         uint32_t fa[8][4], fb[8][2];
-        const float* yp = s_y + (ONE ? 0 : g) * pitch + (k - i0) * PQ_STRIDE + warp * 128 + 16 * t4;
+        const float* yp = s_y + g * pitch + (k - i0) * PQ_STRIDE + warp * 128 + 16 * t4;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (ONE || g < a.B) x = *reinterpret_cast<const float4*>(yp + 64 * (s >> 2) + 4 * (s & 3));
-          a_words<ONE>(x.x, x.y, g, fa[s][0], fa[s][1], fb[s][0]);
-          a_words<ONE>(x.z, x.w, g, fa[s][2], fa[s][3], fb[s][1]);
+          if (g < a.B) x = *reinterpret_cast<const float4*>(yp + 64 * (s >> 2) + 4 * (s & 3));
+          split3(x.x, x.y, fa[s][0], fa[s][1], fb[s][0]);
+          split3(x.z, x.w, fa[s][2], fa[s][3], fb[s][1]);
         }
         copies_wait<PQ_SLOTS - 1>();
         const char* w = mine + slot * PQ_SLOT + g * PQ_PITCH + t4 * 32;
@@ -250,11 +415,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
               if (s == 0) mma_bf16_first(c[i], fa[s], b0, b1);
               else mma_bf16(c[i], fa[s], b0, b1);
             }
-            if constexpr (!ONE) {
-              const uint32_t low[4] = {0u, fb[s][0], 0u, fb[s][1]};
+            const uint32_t low[4] = {0u, fb[s][0], 0u, fb[s][1]};
 #pragma unroll
-              for (int i = 0; i < PQ_TILES; ++i) mma_bf16(c[i], low, h ? v[i].z : v[i].x, h ? v[i].w : v[i].y);
-            }
+            for (int i = 0; i < PQ_TILES; ++i) mma_bf16(c[i], low, h ? v[i].z : v[i].x, h ? v[i].w : v[i].y);
           }
         }
 #pragma unroll
@@ -269,54 +432,23 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
 #pragma unroll
       for (int i = 0; i < PQ_TILES; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = acc[i][e];
-          if constexpr (ONE) v += __shfl_xor_sync(0xffffffffu, v, 4);
-          if (!ONE || g == 0) red[warp][8 * i + 2 * t4 + e][ONE ? 0 : g] = v;
-        }
+        for (int e = 0; e < 2; ++e) red[warp][8 * i + 2 * t4 + e][g] = acc[i][e];
       __syncthreads();
       if (tid < PQ_TILES * 8 * QR) {
         const int r = tid % (PQ_TILES * 8), b = tid / (PQ_TILES * 8), i = r >> 3, t = t0 + pass * nt + i;
         if (i < nt && t < t1 && b < a.B) {
-          const Tile p = tile_at(t);
+          const QkvTile p = qkv_tile(a, nsel, s_rest, t);
           if (p.head >= 0) {
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < PP_WARPS; ++w) v += red[w][r][b];
-            const int c = p.c + (r & 7);
-            if (a.bias) v += a.bias[(size_t)(p.head * 3 + p.m) * a.dh + c];
-            if (p.m == 0) {
-              a.q[((size_t)b * a.kh_max + p.j) * a.dh + c] = v;
-            } else {
-              const int slot = a.slots[b];
-              if (slot >= 0 && slot < a.n_slots) {
-                const int pg = slot / a.page;
-                const long long row = (long long)pg * a.stride_rows + p.head * a.page + (slot - pg * a.page);
-                (p.m == 1 ? a.K : a.V)[row * a.dh + c] = __float2bfloat16_rn(v);
-              } else if (slot >= 0) {
-                raise_status(a.status, ST_RANGE);
-              }
-            }
+            qkv_store(a, p, b, p.c + (r & 7), v);
           }
         }
       }
     }
   }
-  if (!a.all) {
-    const int n = s_nrest * a.B, vecs = a.dh >> 3;  // (head, request) pairs, 16-byte vectors of each
-    for (int x = blockIdx.x * PP_THREADS + tid; x < n * vecs; x += gridDim.x * PP_THREADS) {
-      const int pr = x / vecs, v = x - pr * vecs, b = pr % a.B, head = s_rest[pr / a.B];
-      const int slot = a.slots[b];
-      if (slot < 0 || slot >= a.n_slots) {
-        if (slot >= 0) raise_status(a.status, ST_RANGE);
-        continue;
-      }
-      const int pg = slot / a.page;
-      const long long row = (long long)pg * a.stride_rows + head * a.page + (slot - pg * a.page);
-      reinterpret_cast<uint4*>(a.K)[row * vecs + v] = make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(a.V)[row * vecs + v] = make_uint4(0, 0, 0, 0);
-    }
-  }
+  if (!a.all) qkv_clear(a, s_rest, s_nrest);
 }
 
 // ----------------------------------------------------------------------------

@@ -447,7 +447,8 @@ def test_sparse_mha_paged_matches_the_model(wdt, B, dh, heads, exact, acc, bias)
 @pytest.mark.parametrize("B, d, h, heads, exact", [
     (7, 5000, 32, list(range(32)), False),  # channels in segments, weight tiles in several passes, odd blocks
     (2, 20480, 3, [0, 2], True),            # more column blocks of W^O than SMs
-    (1, 12296, 40, list(range(0, 40, 2)), False), (3, 264, 8, [7], True), (8, 1032, 5, [0, 1, 2, 3, 4], False)])
+    (1, 12296, 40, list(range(0, 40, 2)), False), (1, 1000, 64, list(range(64)), False), (1, 4104, 40, [3, 39], True),
+    (3, 264, 8, [7], True), (8, 1032, 5, [0, 1, 2, 3, 4], False)])
 def test_sparse_mha_paged_at_sizes_that_do_not_divide(B, d, h, heads, exact):
     dh, page = 64, 12
     g = gen(d)
