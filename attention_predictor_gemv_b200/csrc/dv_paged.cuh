@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
   constexpr int AF = ONE ? 1 : WIDE ? 3 : 2;  // A fragments that hold the terms of q, and of p
   constexpr int QH = WIDE ? 2 : 1;  // query rows of a lane: g, and g + 8
   constexpr int NK = 4 * NB;        // MMA steps over the channels
-  constexpr int EN = F32 ? 2 : 4;  // channel tiles whose products run side by side
+  constexpr int EN = F32 || NB * QR >= 32 ? 2 : 4;  // channel tiles whose products run side by side
   extern __shared__ __align__(16) char smem_raw[];
   __shared__ unsigned sc[WARPS + 1];
   // items that cross warps or CTAs: first unit (-1: none), unit behind the last, row, item. 0..7: left open by that
