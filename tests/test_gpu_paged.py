@@ -402,7 +402,7 @@ def mha_model(t, y, Kf, Vf, table, lens, slots, heads, scale, page, exact, bias)
 @pytest.mark.parametrize("B, dh, heads, exact, acc, bias", [
     (1, 64, [0, 3], False, False, True), (1, 128, [2], True, True, False), (4, 64, [0, 1, 2, 3], False, True, True),
     (3, 128, [1, 3], True, False, True), (8, 64, [0, 2], False, False, True), (16, 64, [1], True, True, False),
-    (2, 64, [], False, False, True), (2, 64, [], False, True, False)])
+    (2, 64, [], False, False, True), (2, 64, [], False, True, False), (2, 64, [], True, False, True)])
 def test_sparse_mha_paged_matches_the_model(wdt, B, dh, heads, exact, acc, bias):
     d, h, page = 512, 4, 16
     s = wl.LayerShape(d=d, N=1024, r=32, h=h, dh=dh, L=8, cap=9, B=1, wdtype=wdt, kvdtype=wdt)
@@ -448,7 +448,7 @@ def test_sparse_mha_paged_matches_the_model(wdt, B, dh, heads, exact, acc, bias)
     (7, 5000, 32, list(range(32)), False),  # channels in segments, weight tiles in several passes, odd blocks
     (2, 20480, 3, [0, 2], True),            # more column blocks of W^O than SMs
     (1, 12296, 40, list(range(0, 40, 2)), False), (1, 1000, 64, list(range(64)), False), (1, 4104, 40, [3, 39], True),
-    (3, 264, 8, [7], True), (8, 1032, 5, [0, 1, 2, 3, 4], False)])
+    (3, 264, 8, [7], True), (8, 1032, 5, [0, 1, 2, 3, 4], False), (1, 8, 2, [1], False), (5, 16, 2, [0], True)])
 def test_sparse_mha_paged_at_sizes_that_do_not_divide(B, d, h, heads, exact):
     dh, page = 64, 12
     g = gen(d)
@@ -457,6 +457,9 @@ def test_sparse_mha_paged_at_sizes_that_do_not_divide(B, d, h, heads, exact):
     bqkv = 0.3 * torch.randn(h, 3, dh, generator=g, device="cuda")
     lens = [(29 * (b + 1)) % 60 + 1 for b in range(B)]
     K, V, table, lens_t = make_cache(lens, h, dh, page, BF16, B)
+    pool = torch.full((K.shape[0], 2, h, page, dh), float("nan"), device="cuda", dtype=BF16)  # K and V share a pool
+    pool[:, 0], pool[:, 1] = K, V
+    K, V = pool[:, 0], pool[:, 1]
     slots = [int(table[b, (n - 1) // page]) * page + (n - 1) % page for b, n in enumerate(lens)]
     y = torch.randn(B, d, generator=g, device="cuda")
     out = torch.full((B, d), 7.0, device="cuda")
@@ -487,6 +490,47 @@ def test_sparse_mha_paged_at_sizes_that_do_not_divide(B, d, h, heads, exact):
             want[b] += (torch.softmax((k @ qkv[b, i, 0]) * 0.125, 0) @ v) @ WOt[i].double()
     # 64 len(heads) terms a sum, each of fp32 operands in three bf16 terms: far inside 2^-16 of the result's norm
     assert (out.double() - want).norm() <= 2.0 ** -16 * want.norm()
+
+
+def test_a_block_captured_and_replayed_follows_its_inputs():
+    """One captured dv_sparse_mha_paged, replayed after the lengths, slots, set and input changed in place."""
+    d, h, dh, page, B = 512, 6, 64, 8, 3
+    g = gen(77)
+    W = (torch.randn(h, 3, dh, d, generator=g, device="cuda") * d ** -0.5).to(BF16)
+    WOt = (torch.randn(h, dh, d, generator=g, device="cuda") * d ** -0.5).to(BF16)
+    full = [70, 9, 33]
+    K, V, table, lens = make_cache(full, h, dh, page, BF16, 5, junk=0.0)
+    kv, kh = bd.PagedKV(K, V), 4
+    y, out = torch.randn(B, d, generator=g, device="cuda"), torch.empty(B, d, device="cuda")
+    slots, idx, cnt = i32([-1] * B), i32([0, 1, 2, 3]), i32([4])
+    wss = [bd.workspace(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=B, d=d, h=h, dh=dh, kh_max=kh)) for _ in range(2)]
+
+    def call(o, ws):
+        bd.dv_sparse_mha_paged(y, W, None, WOt, None, kv, table, lens, slots, 0.125, idx, cnt, kh, o, ws)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(out, wss[0])
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            call(out, wss[0])
+    torch.cuda.current_stream().wait_stream(side)
+    for it, (ln, heads) in enumerate([([70, 9, 33], [0, 1, 2, 3]), ([12, 0, 33], [2, 5]), ([1, 8, 17], [4]), ([64, 9, 0], [])]):
+        lens.copy_(i32(ln))
+        slots.copy_(i32([int(table[b, (n - 1) // page]) * page + (n - 1) % page if n else -1 for b, n in enumerate(ln)]))
+        idx[: len(heads)] = i32(heads)
+        cnt.copy_(i32([len(heads)]))
+        y.copy_(torch.randn(B, d, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        again = torch.empty_like(out)
+        call(again, wss[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, again)  # the same sums in the same order, whatever the launch
+        if not heads:
+            assert not out.any()
+    assert all(bd.dv_read_device_status(ws) == 0 for ws in wss)
 
 
 def test_paged_block_equals_the_contiguous_one():
