@@ -120,20 +120,111 @@ __device__ __forceinline__ QkvTile qkv_tile(const PagedQkvArgs& a, int nsel, con
   return p;
 }
 
-// One sum to its place: q to the workspace, k and v, rounded once, to their pages
-__device__ __forceinline__ void qkv_store(const PagedQkvArgs& a, const QkvTile& p, int b, int c, float v) {
-  if (a.bias) v += a.bias[(size_t)(p.head * 3 + p.m) * a.dh + c];
-  if (p.m == 0) {
-    a.q[((size_t)b * a.kh_max + p.j) * a.dh + c] = v;
-    return;
+// Values of k and v next to a rounding border.
+//
+// One bf16 step of one stored value moves the output by up to 2e-4 of its norm where few keys are attended to, and fp32
+// sums in another order fall on the other side of a border for one value in some thousands. So k and v are what the
+// exact sum gives, rounded to fp32 and then to bf16, whatever the kernel's form or the number of requests: a sum so
+// close to a border that its own error could decide is formed again in 64 bits, its row read once more. The sums'
+// errors are 1.4e-7 of a value's spread in the mean square (2048 to 12288 channels); the magnitudes of the eight
+// warps' partial sums, added, are 2.3 times that spread for independent terms, and 2^-21 of it is 7 times the error.
+// About one value in 400 is formed again, by the whole CTA at its end, about 2 us each where 12288 channels: four requests
+// of 4096 channels 49 us a call for 46 without it, one of 12288 channels 53.5 us for 52. By a warp each, at once, these
+// took 53 and 64 us; with the rows' loads through shared memory, all at once, the same; with the loop unrolled by three
+// the first took a microsecond more.
+constexpr int QC_ENTRIES = PP_THREADS + 128, QC_ROUND = 32;
+struct QkvClose {
+  long long to[QC_ENTRIES];  // the value's element of its pool, doubled, odd: of V
+  int row[QC_ENTRIES], b[QC_ENTRIES];
+  double sum[QC_ROUND][PP_WARPS];
+  int n;
+};
+
+// Entries' values in 64 bits (products are exact there): each warp takes every eighth 256 channels.
+__device__ __forceinline__ void qkv_again(const PagedQkvArgs& a, QkvClose& s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = s.n;
+  for (int i0 = 0; i0 < n; i0 += QC_ROUND) {
+    const int m = min(QC_ROUND, n - i0);
+#pragma unroll 1
+    for (int i = 0; i < m; ++i) {
+      const __nv_bfloat16* w = a.W + (size_t)s.row[i0 + i] * a.d;
+      const float* y = a.y + (size_t)s.b[i0 + i] * a.d;
+      double part[8] = {};
+#pragma unroll 1
+      for (int c = 256 * warp + 8 * lane; c < a.d; c += 256 * PP_WARPS) {
+        const uint4 u = *reinterpret_cast<const uint4*>(w + c);
+        const float4 y0 = *reinterpret_cast<const float4*>(y + c), y1 = *reinterpret_cast<const float4*>(y + c + 4);
+        const float ys[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = word_of(u, e >> 1);
+          part[e] = fma((double)__uint_as_float(e & 1 ? x & 0xffff0000u : x << 16), (double)ys[e], part[e]);
+        }
+      }
+      double sum = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) s.sum[i][warp] = sum;
+    }
+    __syncthreads();
+    if (tid < m) {
+      double v = a.bias ? (double)a.bias[s.row[i0 + tid]] : 0.0;
+#pragma unroll
+      for (int w = 0; w < PP_WARPS; ++w) v += s.sum[tid][w];
+      const long long to = s.to[i0 + tid];
+      (to & 1 ? a.V : a.K)[to >> 1] = __float2bfloat16_rn((float)v);
+    }
+    __syncthreads();
   }
-  const int slot = a.slots[b];
-  if (slot >= 0 && slot < a.n_slots) {
+  if (tid == 0) s.n = 0;
+}
+
+// Where a sum goes: m 0 to q, 1 to K, 2 to V, at element `to`; -1: nowhere. Formed before the sum, since the loads that it
+// and the bias need follow one another.
+struct QkvPlace {
+  int m, row;  // (weight row)
+  long long to;
+  float bias;
+};
+
+__device__ __forceinline__ QkvPlace qkv_place(const PagedQkvArgs& a, const QkvTile& p, int b, int slot, int r) {
+  QkvPlace t = {-1, 0, 0, 0.f};
+  if (p.head < 0) return t;
+  const int c = p.c + r;
+  t.row = (p.head * 3 + p.m) * a.dh + c;
+  if (a.bias) t.bias = a.bias[t.row];
+  if (p.m == 0) {
+    t.m = 0;
+    t.to = ((long long)b * a.kh_max + p.j) * a.dh + c;
+  } else if (slot >= 0 && slot < a.n_slots) {
     const int pg = slot / a.page;
-    const long long row = (long long)pg * a.stride_rows + p.head * a.page + (slot - pg * a.page);
-    (p.m == 1 ? a.K : a.V)[row * a.dh + c] = __float2bfloat16_rn(v);
+    t.m = p.m;
+    t.to = ((long long)pg * a.stride_rows + p.head * a.page + (slot - pg * a.page)) * a.dh + c;
   } else if (slot >= 0) {
     raise_status(a.status, ST_RANGE);
+  }
+  return t;
+}
+
+// A value to its place: the sum of the warps' partial sums, `step` floats apart, and the bias
+__device__ __forceinline__ void qkv_store(const PagedQkvArgs& a, const QkvPlace& t, int b, const float* part, int step, QkvClose& s) {
+  float v = 0.f, mag = 0.f;
+#pragma unroll
+  for (int w = 0; w < PP_WARPS; ++w) {
+    const float x = part[w * step];
+    v += x;
+    mag += fabsf(x);
+  }
+  v += t.bias;
+  if (t.m == 0) a.q[t.to] = v;
+  if (t.m <= 0) return;
+  (t.m == 1 ? a.K : a.V)[t.to] = __float2bfloat16_rn(v);
+  const float border = __uint_as_float((__float_as_uint(v) & 0xffff0000u) | 0x8000u);
+  if (fabsf(v - border) <= (mag + fabsf(v)) * 0x1p-21f) {
+    const int i = atomicAdd(&s.n, 1);
+    s.to[i] = 2 * t.to + (t.m == 2);
+    s.row[i] = t.row;
+    s.b[i] = b;
   }
 }
 
@@ -163,18 +254,21 @@ constexpr int PT_CW = 512, PT_PITCH = 2 * PT_CW + 16, PT_SLOT = 8 * PT_PITCH, PT
 constexpr int PT_HOLD = 8;  // tiles whose sums are kept before the warps' are added
 constexpr int PT_RING = PP_WARPS * PT_SLOTS * PT_SLOT, PT_RED = PT_HOLD * PP_WARPS * 8 * 4;
 constexpr size_t paged_qkv_one_smem() { return PT_RING + PT_RED + 3 * 2 * (PT_MAX_D + 8); }
-static_assert(paged_qkv_one_smem() + 2 * PTK_MAX_H + 4 * PQ_MAX_TILES + 1024 <= 227 * 1024, "shared memory");
+static_assert(paged_qkv_one_smem() + 2 * PTK_MAX_H + 4 * PQ_MAX_TILES + sizeof(QkvClose) + 1024 <= 227 * 1024, "shared memory");
 
 __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_one_kernel(PagedQkvArgs a) {
   constexpr int CW = PT_CW, SLOTS = PT_SLOTS, PITCH = PT_PITCH, CPR = CW / 8;  // 16-byte pieces of a row
   extern __shared__ __align__(16) char ring[];
   __shared__ short s_rest[PTK_MAX_H];
   __shared__ int s_nrest, s_row[PQ_MAX_TILES];  // a tile's first weight row, -1: none
+  __shared__ QkvClose s_close;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   float* red = reinterpret_cast<float*>(ring + PP_WARPS * SLOTS * PT_SLOT);  // [tiles held][warps][8 rows]
   __nv_bfloat16* s_y = reinterpret_cast<__nv_bfloat16*>(ring + PP_WARPS * SLOTS * PT_SLOT + PT_RED);
+  if (tid == 0) s_close.n = 0;
   griddep_wait();
   griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
+  const int slot_of = a.slots[0];
   const int nsel = qkv_lists(a, s_rest, &s_nrest);
   const int tiles = (nsel * 3 + (a.all ? s_nrest * 2 : 0)) * (a.dh >> 3);
   const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x), t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
@@ -228,6 +322,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_one_kernel(PagedQkvAr
 #pragma unroll 1
   for (int ta = t0; ta < t1; ta += PT_HOLD) {
     const int held = min(PT_HOLD, t1 - ta);
+    QkvPlace place = {-1, 0, 0, 0.f};
+    if (tid < held * 8) place = qkv_place(a, qkv_tile(a, nsel, s_rest, ta + (tid >> 3)), 0, slot_of, tid & 7);
 #pragma unroll 1
     for (int i = 0; i < held; ++i) {
       float acc[2] = {0.f, 0.f};
@@ -267,17 +363,12 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_one_kernel(PagedQkvAr
       }
     }
     __syncthreads();
-    if (tid < held * 8) {
-      const int r = tid & 7, i = tid >> 3;
-      const QkvTile p = qkv_tile(a, nsel, s_rest, ta + i);
-      if (p.head >= 0) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < PP_WARPS; ++w) v += red[(i * PP_WARPS + w) * 8 + r];
-        qkv_store(a, p, 0, p.c + r, v);
-      }
-    }
+    if (place.m >= 0) qkv_store(a, place, 0, red + (tid >> 3) * PP_WARPS * 8 + (tid & 7), 8, s_close);
     __syncthreads();
+    if (s_close.n > QC_ENTRIES - PP_THREADS || ta + PT_HOLD >= t1) {
+      qkv_again(a, s_close);
+      __syncthreads();
+    }
   }
   if (!a.all) qkv_clear(a, s_rest, s_nrest);
 }
@@ -292,7 +383,7 @@ constexpr int PQ_YF = 16384;                             // floats of y at a tim
 constexpr int PQ_YPAD = 4;                               // of each request's row, in floats
 constexpr size_t PQ_RING = (size_t)PP_WARPS * PQ_SLOTS * PQ_SLOT;
 constexpr size_t paged_qkv_smem() { return PQ_RING + 4 * (PQ_YF + PP_MAX_B * PQ_YPAD); }
-static_assert(paged_qkv_smem() + 2 * PTK_MAX_H + PP_WARPS * PQ_TILES * 8 * 9 * 4 + 4 * PQ_MAX_TILES + 1024 <= 227 * 1024, "shared memory");
+static_assert(paged_qkv_smem() + 2 * PTK_MAX_H + PP_WARPS * PQ_TILES * 8 * 9 * 4 + 4 * PQ_MAX_TILES + sizeof(QkvClose) + 1024 <= 227 * 1024, "shared memory");
 
 __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a) {
   constexpr int QR = PP_MAX_B;
@@ -300,7 +391,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
   __shared__ short s_rest[PTK_MAX_H];
   __shared__ float red[PP_WARPS][PQ_TILES * 8][QR + 1];
   __shared__ int s_nrest, s_row[PQ_MAX_TILES];  // a tile's first weight row, -1: none
+  __shared__ QkvClose s_close;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  if (tid == 0) s_close.n = 0;
   griddep_wait();
   griddep_launch();  // (after the wait: what starts early finds everything before this call complete)
 
@@ -318,6 +411,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
   };
   request_y(0);
 
+  const int b_of = tid / (PQ_TILES * 8), slot_of = a.slots[min(b_of, a.B - 1)];  // the request whose sums this thread stores
   const int nsel = qkv_lists(a, s_rest, &s_nrest);
   const int tiles = (nsel * 3 + (a.all ? s_nrest * 2 : 0)) * (a.dh >> 3);
   const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x), t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
@@ -375,6 +469,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
     int slot = 0;
     for (int pass = 0; pass < passes; ++pass) {
       float acc[PQ_TILES][2] = {};
+      QkvPlace place = {-1, 0, 0, 0.f};
+      {
+        const int i = (tid >> 3) % PQ_TILES, t = t0 + pass * nt + i;
+        if (i < nt && t < t1 && b_of < a.B) place = qkv_place(a, qkv_tile(a, nsel, s_rest, t), b_of, slot_of, tid & 7);
+      }
       for (int i0 = 0; i0 * PQ_STRIDE < a.d; i0 += seg) {
         if (pass + i0 == 0) {  // the first segment: all but the ring's groups
           copies_wait<PQ_SLOTS - 1>();
@@ -428,23 +527,17 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
         __syncwarp();  // the slot is free
       }
       }
-      if (pass > 0) __syncthreads();  // (the last pass's sums are read)
 #pragma unroll
       for (int i = 0; i < PQ_TILES; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) red[warp][8 * i + 2 * t4 + e][g] = acc[i][e];
       __syncthreads();
-      if (tid < PQ_TILES * 8 * QR) {
-        const int r = tid % (PQ_TILES * 8), b = tid / (PQ_TILES * 8), i = r >> 3, t = t0 + pass * nt + i;
-        if (i < nt && t < t1 && b < a.B) {
-          const QkvTile p = qkv_tile(a, nsel, s_rest, t);
-          if (p.head >= 0) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < PP_WARPS; ++w) v += red[w][r][b];
-            qkv_store(a, p, b, p.c + (r & 7), v);
-          }
-        }
+      static_assert(PQ_TILES * 8 * QR == PP_THREADS, "a sum each");
+      if (place.m >= 0) qkv_store(a, place, b_of, &red[0][tid % (PQ_TILES * 8)][b_of], PQ_TILES * 8 * (QR + 1), s_close);
+      __syncthreads();
+      if (s_close.n > QC_ENTRIES - PP_THREADS || pass + 1 == passes) {
+        qkv_again(a, s_close);
+        __syncthreads();
       }
     }
   }

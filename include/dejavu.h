@@ -519,7 +519,12 @@ DV_API dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int
  * for dv_sparse_mha (h = kv->h_kv heads, dh 64 or 128, kv->kvdtype = wdtype,
  * h <= 1024). exact_kv nonzero: k and v of the unselected heads are computed
  * and stored too; 0: their place in slots[b] is set to zero, since a recycled page
- * holds another request's keys and values. A row of length 0 gets bO alone. */
+ * holds another request's keys and values. A row of length 0 gets bO alone.
+ * The attention reads k and v of the new token as they are stored. Where few
+ * keys are attended to, one bf16 step of one of them moves out by up to 2e-4 of
+ * its norm, so with bf16 weights and B <= 8 they are the exact sums, rounded to
+ * fp32 and then to bf16, for any B and set; sums in another order (a plain fp32
+ * matrix product's, the contiguous call's) may store a neighbouring value. */
 DV_API dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, const float* bqkv,
                                      const void* WOt, const float* bO, dv_dtype wdtype, const dv_paged_kv* kv,
                                      const int32_t* table, int W, const int32_t* lens, const int32_t* slots,

@@ -492,6 +492,92 @@ def test_sparse_mha_paged_at_sizes_that_do_not_divide(B, d, h, heads, exact):
     assert (out.double() - want).norm() <= 2.0 ** -16 * want.norm()
 
 
+def block_case(B, d, h, dh, heads, lens, seed, page=8, dtype=BF16, bias=True):
+    """Inputs of the attention block over pages, in one dict; the pool's slots past the lengths hold NaN."""
+    g = gen(seed)
+    K, V, table, lens_t = make_cache(lens, h, dh, page, dtype, seed)
+    return dict(
+        y=torch.randn(B, d, generator=g, device="cuda"), Wqkv=(torch.randn(h, 3, dh, d, generator=g, device="cuda") * d ** -0.5).to(dtype),
+        WOt=(torch.randn(h, dh, d, generator=g, device="cuda") * d ** -0.5).to(dtype),
+        bqkv=0.3 * torch.randn(h, 3, dh, generator=g, device="cuda") if bias else None,
+        bO=0.3 * torch.randn(d, generator=g, device="cuda") if bias else None, K=K, V=V, table=table, lens=lens_t, page=page, heads=heads,
+        slots=i32([int(table[b, (n - 1) // page]) * page + (n - 1) % page if n > 0 else -1 for b, n in enumerate(lens)]))
+
+
+def run_block(c, ws=None, exact=False, accumulate=False, out=None, idx=None, count=None, kh=None):
+    B, d = c["y"].shape
+    h, dh = c["K"].shape[1], c["K"].shape[3]
+    idx = c["heads"] if idx is None else idx
+    kh = len(idx) if kh is None else kh
+    ws = bd.workspace(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=B, d=d, h=h, dh=dh, kh_max=kh)) if ws is None else ws
+    out = torch.full((B, d), 7.0, device="cuda") if out is None else out
+    bd.dv_sparse_mha_paged(c["y"], c["Wqkv"], c["bqkv"], c["WOt"], c["bO"], bd.PagedKV(c["K"], c["V"]), c["table"], c["lens"], c["slots"],
+                           dh ** -0.5, i32(list(idx) + [0]), i32([len(idx) if count is None else count]), kh, out, ws, accumulate=accumulate,
+                           exact_kv=exact)
+    torch.cuda.synchronize()
+    return out, bd.dv_read_device_status(ws)
+
+
+def block_sums(c):
+    """(q, k, v) of every head [B][h][3][dh] in 64 bits, bias included, and the sum of their terms' magnitudes."""
+    y, W = c["y"].double(), c["Wqkv"].double()
+    s, m = torch.einsum("bd,hmcd->bhmc", y, W), torch.einsum("bd,hmcd->bhmc", y.abs(), W.abs())
+    return (s, m) if c["bqkv"] is None else (s + c["bqkv"].double(), m + c["bqkv"].double().abs())
+
+
+def block_out(c, q):
+    """The block's output in 64 bits, from q [B][h][dh] and the keys and values that the pages hold now."""
+    out = torch.zeros_like(c["y"], dtype=torch.float64)
+    for b, n in enumerate(c["lens"].tolist()):
+        if n > 0:
+            pages = c["table"][b, : -(-n // c["page"])].long()
+            for i in c["heads"]:
+                k, v = (c[x][pages, i].reshape(-1, q.shape[2])[:n].double() for x in "KV")
+                out[b] += (torch.softmax((k @ q[b, i]) * q.shape[2] ** -0.5, 0) @ v) @ c["WOt"][i].double()
+    return out if c["bO"] is None else out + c["bO"].double()
+
+
+@pytest.mark.parametrize("B, d, h, dh, n", [(1, 4096, 32, 128, 2), (1, 2048, 32, 64, 1), (2, 2048, 24, 64, 3), (3, 4096, 32, 128, 2),
+                                            (4, 4096, 20, 128, 4), (5, 1000, 40, 64, 8), (8, 2048, 32, 64, 2), (1, 12296, 12, 128, 5)])
+@pytest.mark.parametrize("seed", range(4))
+def test_a_block_stores_what_the_exact_sums_round_to(B, d, h, dh, n, seed):
+    """With few keys one bf16 step of one stored value moves the output by more than all its fp32 sums' errors, so the
+    stored values must not depend on how a sum was formed: they are the 64-bit sums rounded to fp32, then to bf16, every
+    one. (Only a sum within 2^-40 of its terms of an fp32 border that decides might not be: one in 10^9.)"""
+    c = block_case(B, d, h, dh, list(range(h)), [max(1, n - b % 2) for b in range(B)], 100 * seed + B + d)
+    sums, _ = block_sums(c)
+    out, status = run_block(c)
+    assert status == 0
+    want = sums.float().to(BF16)
+    for b, sl in enumerate(c["slots"].tolist()):
+        p, o = divmod(sl, c["page"])
+        assert torch.equal(c["K"][p, :, o], want[b, :, 1]) and torch.equal(c["V"][p, :, o], want[b, :, 2])
+    # and so the output is within fp32 rounding of the definition's: chains of at most 24 tensor core steps, the scores' and
+    # the weights' a few more, each off by 2^-23 of its partial sum at most: 64 of them
+    ref = block_out(c, sums[:, :, 0])
+    assert (out.double() - ref).norm() <= 64 * 2.0 ** -23 * ref.norm()
+
+
+@pytest.mark.parametrize("B, h", [(1, 128), (8, 40), (5, 128)])
+def test_a_block_whose_sums_all_lie_at_a_border(B, h):
+    """Every k and v is 257, half way between two bf16 values, or 2^-12 to either side of it."""
+    d, dh = 64, 128
+    c = block_case(B, d, h, dh, list(range(h)), [3] * B, 5, bias=False)
+    c["y"].fill_(0.0)
+    c["y"][:, :3] = torch.tensor([2.0, 0.5, 2.0 ** -6], device="cuda")
+    c["y"] *= torch.where(torch.arange(B, device="cuda") % 2 == 0, 1.0, -1.0)[:, None]
+    c["Wqkv"][..., 0], c["Wqkv"][..., 1] = 128.0, 2.0
+    c["Wqkv"][..., 2] = (torch.randint(-1, 2, (h, 3, dh), generator=gen(6), device="cuda") * 2.0 ** -6).to(BF16)
+    sums, _ = block_sums(c)
+    assert set(sums.abs().unique().tolist()) == {257 - 2.0 ** -12, 257.0, 257 + 2.0 ** -12}
+    _, status = run_block(c)
+    assert status == 0
+    want = sums.float().to(BF16)
+    for b, sl in enumerate(c["slots"].tolist()):
+        p, o = divmod(sl, c["page"])
+        assert torch.equal(c["K"][p, :, o], want[b, :, 1]) and torch.equal(c["V"][p, :, o], want[b, :, 2])
+
+
 def test_a_block_captured_and_replayed_follows_its_inputs():
     """One captured dv_sparse_mha_paged, replayed after the lengths, slots, set and input changed in place."""
     d, h, dh, page, B = 512, 6, 64, 8, 3
