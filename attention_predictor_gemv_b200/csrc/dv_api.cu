@@ -31,7 +31,7 @@ struct Layout {
   size_t status, sel_ticket_h, sel_ticket_m, pa_ticket, pb_ticket, attn_ctr, t1;
   size_t yA, yM, z, scores_h, bm_h, head_idx, head_count, scores, bm_m, idx, count;
   size_t q, part, H, seg_idx, seg_a, seg_cnt, tc_x, tc_act, tc_rowid, tc_tiles, tc_red, tc_tick, tc_acc, total;
-  int nseg, SEG, nsplit_max, KC, XC;
+  int nseg, SEG, nsplit_max, KC, XC, ntick;
 };
 
 bool dims_ok(const dv_dims& D) {
@@ -88,8 +88,10 @@ Layout layout(const dv_dims& D, int wbytes) {
   // reductions: split K of Q/K/V, W1 and the predictor's dense GEMMs, and the
   // row groups of W2 and W^O
   L.tc_red = take(4ull * tc_red_floats(D.k_max, D.kh_max, D.dh, D.d));
-  L.tc_tick = take(4ull * tc_tick_count(D.k_max, D.kh_max, D.dh, D.d));
-  // fixed-point accumulator of the W2 and W^O partial sums [16][d]
+  L.ntick = (int)tc_tick_count(D.k_max, D.kh_max, D.dh, D.d);
+  L.tc_tick = take(4ull * L.ntick);
+  // fixed-point accumulator of the W2 and W^O partial sums [16][d]; like the
+  // tickets it is cleared before each use, since its place goes with the sizes
   L.tc_acc = take(8ull * TC_N * D.d);
   L.total = o;
   return L;
@@ -101,6 +103,11 @@ P* at(void* ws, size_t off) {
 }
 
 dv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DV_OK : DV_ERR_CUDA; }
+
+// What a tensor-core call's split clears: the tickets, or the accumulator of nb rows, or both
+TcClear clear_of(const Layout& L, void* ws, bool tick, int acc_rows, int d) {
+  return {at<unsigned>(ws, L.tc_tick), tick ? L.ntick : 0, at<unsigned long long>(ws, L.tc_acc), acc_rows * d};
+}
 
 #define DV_TRY(expr)                          \
   do {                                        \
@@ -165,7 +172,7 @@ cudaError_t pred_tc(const Layout& L, void* ws, const void* W, int nrows, int K, 
   bf16* xhi = at<bf16>(ws, L.tc_x);
   bf16* xlo = xhi + (size_t)TC_N * L.XC;
   if (split) {  // (not when the previous call split the same x)
-    cudaError_t e = run_tc_split(x, B, K, K, xhi, xlo, K, st);
+    cudaError_t e = run_tc_split(x, B, K, K, xhi, xlo, K, clear_of(L, ws, true, 0, 0), st);
     if (e != cudaSuccess) return e;
   }
   return run_tc_dense(nullptr, 0, nullptr, nullptr, 0, static_cast<const bf16*>(W), nrows, bias, out, ldo, K, xhi, xlo,
@@ -366,7 +373,7 @@ dv_status tc_mlp(const Layout& L, void* ws, const float* y, int B, int d, int N,
   a.acc = at<unsigned long long>(ws, L.tc_acc);
   a.out = out;
   a.status = at<int>(ws, L.status);
-  if (k_max > 0) DV_TRY(run_tc_split(y, B, d, d, xhi, xhi + (size_t)TC_N * L.XC, d, st));
+  DV_TRY(run_tc_split(y, B, k_max > 0 ? d : 0, d, xhi, xhi + (size_t)TC_N * L.XC, d, clear_of(L, ws, true, B, d), st));
   return cuda_status(run_tc_mlp(a, st));
 }
 
@@ -394,7 +401,7 @@ dv_status tc_qkv(const Layout& L, void* ws, const float* y, int B, int d, int h,
   a.status = at<int>(ws, L.status);
   a.red = at<float>(ws, L.tc_red);
   a.tick = at<unsigned>(ws, L.tc_tick);
-  DV_TRY(run_tc_split(y, B, d, d, xhi, xhi + (size_t)TC_N * L.XC, d, st));
+  DV_TRY(run_tc_split(y, B, d, d, xhi, xhi + (size_t)TC_N * L.XC, d, clear_of(L, ws, true, 0, 0), st));
   return cuda_status(run_tc_qkv(a, st));
 }
 
@@ -416,9 +423,8 @@ dv_status tc_wo(const Layout& L, void* ws, int B, int d, int h, int dh, const vo
   a.out = out;
   a.status = at<int>(ws, L.status);
   a.acc = at<unsigned long long>(ws, L.tc_acc);
-  if (kh_max > 0)
-    DV_TRY(run_tc_split(at<float>(ws, L.H), B, kh_max * dh, (long long)kh_max * dh, hhi, hhi + (size_t)TC_N * L.XC,
-                        (long long)kh_max * dh, st));
+  DV_TRY(run_tc_split(at<float>(ws, L.H), B, kh_max * dh, (long long)kh_max * dh, hhi, hhi + (size_t)TC_N * L.XC,
+                      (long long)kh_max * dh, clear_of(L, ws, false, B, d), st));
   return cuda_status(run_tc_wo(a, st));
 }
 
@@ -578,7 +584,7 @@ dv_status layer_begin(const Layout& L, void* ws, const dv_layer_weights* w, cons
     if (tc_h && tc_z) {  // head scores and z in one launch: rows of P_A, then rows of A^T
       bf16* xhi = at<bf16>(ws, L.tc_x);
       bf16* xlo = xhi + (size_t)TC_N * L.XC;
-      DV_TRY(run_tc_split(yA, D.B, D.d, D.d, xhi, xlo, D.d, st));
+      DV_TRY(run_tc_split(yA, D.B, D.d, D.d, xhi, xlo, D.d, clear_of(L, ws, true, 0, 0), st));
       return cuda_status(run_tc_dense(static_cast<const bf16*>(ahead->w->PA), D.h, nullptr, ahead->sh, D.h,
                                       static_cast<const bf16*>(ahead->w->At), D.r, nullptr, ahead->z, D.r, D.d, xhi,
                                       xlo, D.B, at<float>(ws, L.tc_red), at<unsigned>(ws, L.tc_tick), status, st));

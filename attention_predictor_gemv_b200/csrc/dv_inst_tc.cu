@@ -113,8 +113,8 @@ size_t tc_tick_count(int k_max, int kh_max, int dh, int d) {
 }
 
 namespace {
-// out[b][:] += the fixed-point totals in acc (+ bias); acc back to zero
-cudaError_t run_tc_finalize(unsigned long long* acc, const float* bias, float* out, int nb, int d, cudaStream_t st) {
+// out[b][:] += the fixed-point totals in acc (+ bias)
+cudaError_t run_tc_finalize(const unsigned long long* acc, const float* bias, float* out, int nb, int d, cudaStream_t st) {
   TcFinalizeArgs f{acc, bias, out, nb, d};
   const long long n = (long long)nb * d, cap = 2ll * sm_count();
   const long long g = (n + 255) / 256;
@@ -123,8 +123,8 @@ cudaError_t run_tc_finalize(unsigned long long* acc, const float* bias, float* o
 }  // namespace
 
 cudaError_t run_tc_split(const float* x, int nb, int n, long long ld_src, __nv_bfloat16* hi, __nv_bfloat16* lo,
-                         long long ld_dst, cudaStream_t st) {
-  TcSplitArgs a{x, nb, n, ld_src, hi, lo, ld_dst};
+                         long long ld_dst, const TcClear& clear, cudaStream_t st) {
+  TcSplitArgs a{x, nb, n, ld_src, hi, lo, ld_dst, clear};
   const int gx = (n + 255) / 256 < 64 ? (n + 255) / 256 : 64;
   return launch_main(tc_split_kernel, dim3(gx > 0 ? gx : 1, TC_N), dim3(256), 0, st, a);
 }

@@ -452,6 +452,10 @@ __device__ void tc_run(const P& p, int* status, int stages) {
 // ---------------------------------------------------------------------------
 // Activations split into bf16 hi / lo rows: hi[b][j] = bf16(x), lo[b][j] =
 // bf16(x - hi) for b < nb, zero for nb <= b < 16; x = src[b * ld + j].
+//
+// It also clears what the kernels behind it count and add in (TcClear). That
+// lies at offsets that go with the call's sizes, so another call's data may
+// have been there; clearing it at the end of each use is not enough.
 // ---------------------------------------------------------------------------
 struct TcSplitArgs {
   const float* src;
@@ -460,11 +464,15 @@ struct TcSplitArgs {
   __nv_bfloat16* hi;
   __nv_bfloat16* lo;
   long long ld_dst;
+  TcClear clear;
 };
 
 __global__ void __launch_bounds__(256) tc_split_kernel(TcSplitArgs a) {
   griddep_launch();
   griddep_wait();
+  const int first = (blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x, step = gridDim.x * gridDim.y * 256;
+  for (int i = first; i < a.clear.n_tick; i += step) a.clear.tick[i] = 0u;
+  for (int i = first; i < a.clear.n_acc; i += step) a.clear.acc[i] = 0ull;
   const int b = blockIdx.y;
   for (int j = blockIdx.x * 256 + threadIdx.x; j < a.n; j += gridDim.x * 256) {
     const float x = b < a.nb ? a.src[(size_t)b * a.ld_src + j] : 0.f;
@@ -562,9 +570,9 @@ __device__ __forceinline__ bool tc_reduce_parts(float* red, unsigned* tick, int 
 // Order-independent sums of the rowaxpy partials: each partial is rounded to
 // a multiple of 2^-32 and added as a 64-bit integer (two's complement, so an
 // unsigned atomic add), which is exact and associative; tc_finalize_kernel
-// converts each total once (to fp64, exactly, then fp32), adds it and the bias
-// into the output, and zeroes the accumulator. Partials stay far inside the
-// range (|v| < 2^31).
+// converts each total once (to fp64, exactly, then fp32) and adds it and the
+// bias into the output. The accumulator is cleared by the tc_split_kernel before.
+// Partials stay far inside the range (|v| < 2^31).
 // ---------------------------------------------------------------------------
 constexpr double TC_FIXED_SCALE = 4294967296.0;  // 2^32
 
@@ -578,7 +586,7 @@ __device__ __forceinline__ void tc_acc_fixed(unsigned long long* acc, int d, int
 }
 
 struct TcFinalizeArgs {
-  unsigned long long* acc;  // [nb][d], zero on exit
+  const unsigned long long* acc;  // [nb][d]
   const float* bias;        // [d] or null
   float* out;               // [nb][d], accumulated into
   int nb, d;
@@ -589,8 +597,7 @@ __global__ void __launch_bounds__(256) tc_finalize_kernel(TcFinalizeArgs a) {
   griddep_wait();
   const int n = a.nb * a.d;
   for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-    const long long q = (long long)a.acc[i];
-    a.acc[i] = 0ull;
+    const long long q = (long long)__ldcg(a.acc + i);
     const int col = i % a.d;
     a.out[i] += (float)((double)q / TC_FIXED_SCALE) + (a.bias ? a.bias[col] : 0.f);
   }

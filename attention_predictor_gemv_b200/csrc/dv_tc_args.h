@@ -22,6 +22,14 @@ struct TcMaps {
   CUtensorMap w2;  // a second weight matrix (the dense rowdot's second row block)
 };
 
+// Tickets and accumulators that the split of a call's operand clears.
+struct TcClear {
+  unsigned* tick;
+  int n_tick;
+  unsigned long long* acc;
+  int n_acc;
+};
+
 struct TcQkvArgs {
   const __nv_bfloat16* Wqkv;  // [h][3][dh][d]
   const float* bqkv;          // [h][3][dh] or null
@@ -35,7 +43,7 @@ struct TcQkvArgs {
   __nv_bfloat16* Vc;
   int* status;
   float* red;                 // [tiles][parts][16][128] split-K partial sums (parts <= 8)
-  unsigned* tick;             // [tiles] parts finished per tile, zero between calls
+  unsigned* tick;             // [tiles] parts finished per tile, zero on entry
   int stages;                 // ring stages (set by the launcher)
 };
 
@@ -59,8 +67,8 @@ struct TcMlpArgs {
   int* status;
   int act;                   // ACT_RELU or ACT_GELU
   float* red;                // [tiles][parts][16][128] split-K partial sums of W1 (parts <= 8)
-  unsigned* tick;            // [tiles] parts finished per tile, zero between calls
-  unsigned long long* acc;   // [nb][d] fixed-point partial sums of W2, zero between calls
+  unsigned* tick;            // [tiles] parts finished per tile, zero on entry
+  unsigned long long* acc;   // [nb][d] fixed-point partial sums of W2, zero on entry
   int stages;                // ring stages (set by the launcher)
 };
 
@@ -75,7 +83,7 @@ struct TcWoArgs {
   int heads_per_group;
   float* out;                // [nb][d], accumulated into
   int* status;
-  unsigned long long* acc;   // [nb][d] fixed-point partial sums, zero between calls
+  unsigned long long* acc;   // [nb][d] fixed-point partial sums, zero on entry
   int stages;                // ring stages (set by the launcher)
 };
 
@@ -94,7 +102,7 @@ struct TcDenseArgs {
   long long ldo1, ldo2;
   int* status;
   float* red;         // [tiles][2^kslog][16][128] split-K partial sums
-  unsigned* tick;     // [tiles] parts finished per tile, zero between calls
+  unsigned* tick;     // [tiles] parts finished per tile, zero on entry
   int stages;         // ring stages (set by the launcher)
 };
 

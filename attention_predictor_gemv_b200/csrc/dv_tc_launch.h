@@ -25,9 +25,9 @@ int tc_axpy_group(int items_max, int d, int most);
 size_t tc_red_floats(int k_max, int kh_max, int dh, int d);
 size_t tc_tick_count(int k_max, int kh_max, int dh, int d);
 
-// hi / lo bf16 rows [16][ld_dst] of x [nb][n] (row stride ld_src); rows >= nb zero.
+// hi / lo bf16 rows [16][ld_dst] of x [nb][n] (row stride ld_src; n 0: none); rows >= nb zero. Clears what `clear` names.
 cudaError_t run_tc_split(const float* x, int nb, int n, long long ld_src, __nv_bfloat16* hi, __nv_bfloat16* lo,
-                         long long ld_dst, cudaStream_t st);
+                         long long ld_dst, const TcClear& clear, cudaStream_t st);
 cudaError_t run_tc_qkv(TcQkvArgs a, cudaStream_t st);
 // W1 + bias + ReLU with per-tile compaction, then the W2 gather-axpy into out.
 cudaError_t run_tc_mlp(TcMlpArgs a, cudaStream_t st);
@@ -38,8 +38,8 @@ cudaError_t run_tc_wo(TcWoArgs a, cudaStream_t st);
 // rows of W1 [n1][K] (n1 = 0: none), and out2[b][i] = W2[i] . x[b] (+
 // bias2[i]) for the n2 rows of W2, bf16. When the K range is split across
 // CTAs (at most TC_DENSE_PARTS units of tiles x parts) the partial sums go
-// through red [units][128][16] and the per-tile tickets tick (zero between
-// calls).
+// through red [units][128][16] and the per-tile tickets tick (zero on entry,
+// left zero).
 bool tc_dense_ok(int B, int wbytes, int nrows, int K);
 cudaError_t run_tc_dense(const __nv_bfloat16* W1, int n1, const float* bias1, float* out1, long long ldo1,
                          const __nv_bfloat16* W2, int n2, const float* bias2, float* out2, long long ldo2, int K,

@@ -34,8 +34,9 @@
  *  - The workspace is caller-owned device memory of dv_workspace_size() bytes,
  *    zero-filled once before first use. The library leaves its counters at
  *    zero when a call completes, so it needs no clearing between calls; after
- *    an error, zero it again. Two calls that run at the same time must not
- *    share a workspace.
+ *    an error, zero it again. One workspace that is large enough serves calls
+ *    of any operations and sizes one after another. Two calls that run at the
+ *    same time must not share a workspace.
  *  - Batch rows B: 1..16. For B > 1 each selected set is the union of the
  *    rows' sets, and every row is evaluated on the union.
  */
