@@ -126,10 +126,12 @@ __device__ __forceinline__ QkvTile qkv_tile(const PagedQkvArgs& a, int nsel, con
 // sums in another order fall on the other side of a border for one value in some thousands. So k and v are what the
 // exact sum gives, rounded to fp32 and then to bf16, whatever the kernel's form or the number of requests: a sum so
 // close to a border that its own error could decide is formed again in 64 bits, its row read once more. The sums'
-// errors are 1.4e-7 of a value's spread in the mean square (2048 to 12288 channels); the magnitudes of the eight
-// warps' partial sums, added, are 2.3 times that spread for independent terms, and 2^-21 of it is 7 times the error.
+// errors are 1.4e-7 of a value's spread in the mean square (2048 to 12288 channels). The magnitudes of the eight warps'
+// partial sums, added, are 2.3 times that spread for independent terms, but no more than the value itself where one warp
+// has all channels, so the largest of the 32 values that a warp stores is taken: 2 to 4 times the spread, and 2^-22 of it
+// 4 to 7 times the error (fewer channels have smaller errors).
 // About one value in 400 is formed again, by the whole CTA at its end, about 2 us each where 12288 channels: four requests
-// of 4096 channels 49 us a call for 46 without it, one of 12288 channels 53.5 us for 52. By a warp each, at once, these
+// of 4096 channels 48.5 us a call for 46 without it, one of 12288 channels 53.5 us for 52. By a warp each, at once, these
 // took 53 and 64 us; with the rows' loads through shared memory, all at once, the same; with the loop unrolled by three
 // the first took a microsecond more.
 constexpr int QC_ENTRIES = PP_THREADS + 128, QC_ROUND = 32;
@@ -206,21 +208,24 @@ __device__ __forceinline__ QkvPlace qkv_place(const PagedQkvArgs& a, const QkvTi
   return t;
 }
 
-// A value to its place: the sum of the warps' partial sums, `step` floats apart, and the bias
+// A warp's values to their places: each the sum of the warps' partial sums, `step` floats apart, and the bias
 __device__ __forceinline__ void qkv_store(const PagedQkvArgs& a, const QkvPlace& t, int b, const float* part, int step, QkvClose& s) {
   float v = 0.f, mag = 0.f;
+  if (t.m >= 0) {
 #pragma unroll
-  for (int w = 0; w < PP_WARPS; ++w) {
-    const float x = part[w * step];
-    v += x;
-    mag += fabsf(x);
+    for (int w = 0; w < PP_WARPS; ++w) {
+      const float x = part[w * step];
+      v += x;
+      mag += fabsf(x);
+    }
   }
   v += t.bias;
+  mag = __uint_as_float(__reduce_max_sync(0xffffffffu, mag < INFINITY ? __float_as_uint(mag) : 0u));
   if (t.m == 0) a.q[t.to] = v;
   if (t.m <= 0) return;
   (t.m == 1 ? a.K : a.V)[t.to] = __float2bfloat16_rn(v);
   const float border = __uint_as_float((__float_as_uint(v) & 0xffff0000u) | 0x8000u);
-  if (fabsf(v - border) <= (mag + fabsf(v)) * 0x1p-21f) {
+  if (fabsf(v - border) <= (mag + fabsf(v)) * 0x1p-22f) {
     const int i = atomicAdd(&s.n, 1);
     s.to[i] = 2 * t.to + (t.m == 2);
     s.row[i] = t.row;
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_one_kernel(PagedQkvAr
       }
     }
     __syncthreads();
-    if (place.m >= 0) qkv_store(a, place, 0, red + (tid >> 3) * PP_WARPS * 8 + (tid & 7), 8, s_close);
+    if (warp < PT_HOLD / 4) qkv_store(a, place, 0, red + (tid >> 3) * PP_WARPS * 8 + (tid & 7), 8, s_close);
     __syncthreads();
     if (s_close.n > QC_ENTRIES - PP_THREADS || ta + PT_HOLD >= t1) {
       qkv_again(a, s_close);
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_kernel(PagedQkvArgs a
         for (int e = 0; e < 2; ++e) red[warp][8 * i + 2 * t4 + e][g] = acc[i][e];
       __syncthreads();
       static_assert(PQ_TILES * 8 * QR == PP_THREADS, "a sum each");
-      if (place.m >= 0) qkv_store(a, place, b_of, &red[0][tid % (PQ_TILES * 8)][b_of], PQ_TILES * 8 * (QR + 1), s_close);
+      qkv_store(a, place, b_of, &red[0][tid % (PQ_TILES * 8)][b_of], PQ_TILES * 8 * (QR + 1), s_close);
       __syncthreads();
       if (s_close.n > QC_ENTRIES - PP_THREADS || pass + 1 == passes) {
         qkv_again(a, s_close);

@@ -558,6 +558,20 @@ def test_a_block_stores_what_the_exact_sums_round_to(B, d, h, dh, n, seed):
     assert (out.double() - ref).norm() <= 64 * 2.0 ** -23 * ref.norm()
 
 
+@pytest.mark.parametrize("B, d", [(1, 64), (2, 64), (3, 8), (8, 136), (1, 520), (4, 640)])
+def test_a_block_of_few_channels_stores_what_the_exact_sums_round_to(B, d):
+    """Few channels: one warp or two have all of a sum's terms, and a value may be far smaller than they are."""
+    h, dh = 512, 128
+    c = block_case(B, d, h, dh, list(range(h)), [2] * B, d + B)
+    sums, _ = block_sums(c)
+    _, status = run_block(c)
+    assert status == 0
+    want = sums.float().to(BF16)
+    for b, sl in enumerate(c["slots"].tolist()):
+        p, o = divmod(sl, c["page"])
+        assert torch.equal(c["K"][p, :, o], want[b, :, 1]) and torch.equal(c["V"][p, :, o], want[b, :, 2])
+
+
 @pytest.mark.parametrize("B, h", [(1, 128), (8, 40), (5, 128)])
 def test_a_block_whose_sums_all_lie_at_a_border(B, h):
     """Every k and v is 257, half way between two bf16 values, or 2^-12 to either side of it."""
