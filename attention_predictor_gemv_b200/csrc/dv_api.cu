@@ -984,7 +984,7 @@ dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, co
   int* status = at<int>(ws, L.status);
   float *q = at<float>(ws, L.q), *H = at<float>(ws, L.H);
   void *ks = at<char>(ws, P.ks), *vs = at<char>(ws, P.vs);
-  if (paged_proj_ok(B, d, wdtype, h, dh)) {
+  if (paged_proj_ok(B, d, wdtype, h, dh, kh_max, exact_kv != 0)) {
     DV_TRY(run_paged_qkv(kv, Wqkv, bqkv, y, B, d, slots, head_idx, head_count, kh_max, exact_kv != 0, q, status, st));
     if (kh_max > 0)
       DV_TRY(run_paged_attn(kv, q, B, kh_max, 1, table, W, lens, scale, head_idx, head_count, H, nullptr,

@@ -126,9 +126,10 @@ cudaError_t run_paged_token(const dv_paged_kv* kv, const void* ks, const void* v
                                 : launch(paged_token_kernel<float>, grid, dim3(PA_THREADS), 0, st, a);
 }
 
-bool paged_proj_ok(int B, int d, dv_dtype wdtype, int h, int dh) {
-  const int tiles = 3 * h * (dh / 8);  // of 8 weight rows: a CTA lists its share in shared memory
-  return wdtype == DV_BF16 && B <= PP_MAX_B && d % 8 == 0 && dh % 32 == 0 && tiles / sm_count() < PQ_MAX_TILES;
+bool paged_proj_ok(int B, int d, dv_dtype wdtype, int h, int dh, int kh_max, bool all) {
+  // a CTA lists its share of the tiles in shared memory
+  const long long per_cta = (qkv_most_tiles(kh_max, h, dh, all) + sm_count() - 1) / sm_count();
+  return wdtype == DV_BF16 && B <= PP_MAX_B && d % 8 == 0 && dh % 32 == 0 && per_cta <= PQ_MAX_TILES;
 }
 
 cudaError_t run_paged_qkv(const dv_paged_kv* kv, const void* W, const float* bias, const float* y, int B, int d,

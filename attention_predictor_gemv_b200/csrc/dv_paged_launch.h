@@ -48,7 +48,7 @@ cudaError_t run_paged_token(const dv_paged_kv* kv, const void* ks, const void* v
 // weights, at most 8 requests. q, k, v of the selected heads (k and v into
 // their pages, `all`: of every head; else the other heads' places cleared), and
 // W^O, which must follow the attention of this call's set on the stream.
-bool paged_proj_ok(int B, int d, dv_dtype wdtype, int h, int dh);
+bool paged_proj_ok(int B, int d, dv_dtype wdtype, int h, int dh, int kh_max, bool all);
 cudaError_t run_paged_qkv(const dv_paged_kv* kv, const void* W, const float* bias, const float* y, int B, int d,
                           const int32_t* slots, const int32_t* head_idx, const int32_t* head_count, int kh_max, int all,
                           float* q, int* status, cudaStream_t st);

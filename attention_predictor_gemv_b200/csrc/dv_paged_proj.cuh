@@ -250,7 +250,12 @@ __device__ __forceinline__ void qkv_clear(const PagedQkvArgs& a, const short* s_
   }
 }
 
-constexpr int PQ_MAX_TILES = 512;  // of a CTA: 3 * 1024 heads * 16 tiles over 100 SMs or more
+// Tiles of 8 rows that a call can have: q, k, v for every entry of the set, and k, v for every head that no valid entry
+// names (entries out of range or repeated name none, so a set of h entries can leave all h heads to the rest)
+__host__ __device__ constexpr long long qkv_most_tiles(int kh_max, int h, int dh, bool all) {
+  return (3ll * kh_max + (all ? 2ll * h : 0)) * (dh / 8);
+}
+constexpr int PQ_MAX_TILES = 576;  // of a CTA; more on an SM: refused on the host. 1000 entries, 1024 heads of 128 on 148 SMs: 546
 
 // One request: a tile of 8 rows at a time, 512 channels of each row a warp and ring slot, so that what lies together in
 // memory is read together; y's terms, formed once, come from shared memory. For up to 12288 channels: 31 us at the

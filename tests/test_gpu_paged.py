@@ -592,6 +592,21 @@ def test_a_block_whose_sums_all_lie_at_a_border(B, h):
         assert torch.equal(c["K"][p, :, o], want[b, :, 1]) and torch.equal(c["V"][p, :, o], want[b, :, 2])
 
 
+@pytest.mark.parametrize("B", [1, 2, 8])
+@pytest.mark.parametrize("bad", [5000, -1])
+def test_a_block_of_many_heads_whose_set_names_none(B, bad):
+    """The largest tile list: 1000 entries out of range, k and v of all 1024 heads stored."""
+    h, dh, d = 1024, 128, 64
+    c = block_case(B, d, h, dh, [], [1 + b % 2 for b in range(B)], B, page=1)
+    out, status = run_block(c, exact=True, idx=[bad] * 1000)
+    assert status == bd.DV_DEV_INDEX_RANGE
+    sums, _ = block_sums(c)
+    want = sums.float().to(BF16)
+    for b, p in enumerate(c["slots"].tolist()):
+        assert torch.equal(c["K"][p, :, 0], want[b, :, 1]) and torch.equal(c["V"][p, :, 0], want[b, :, 2])
+    assert torch.equal(out, c["bO"].expand(B, d))
+
+
 def test_a_block_captured_and_replayed_follows_its_inputs():
     """One captured dv_sparse_mha_paged, replayed after the lengths, slots, set and input changed in place."""
     d, h, dh, page, B = 512, 6, 64, 8, 3

@@ -3,6 +3,8 @@ device address is fake) and the plain model of the block tables that the GPU
 tests compare with."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -160,3 +162,19 @@ def test_tables_model_grows_shrinks_and_refuses():
     assert m["table"][0] == [0, 2, -1] and m["table"][2] == [3, 4, 1]
     assert m["stack"][:3] == [7, 8, 9] and m["free_count"] == 3
     assert m["slots"] == [2 * 4, 1 * 4] + [-1] * 6 and m["offsets"] == [0, 1, 1, 2, 2, 2]
+
+
+def test_the_projections_tile_list_holds_every_set():
+    """A CTA's list holds its share of the most tiles that a call can have: 1000 entries, none of them a valid head, and k
+    and v of all 1024 heads of 128 channels, over 148 SMs; and the host compares that very count with the list."""
+    here = os.path.join(os.path.dirname(bd.__file__), "csrc")
+    proj, host = (open(os.path.join(here, f)).read() for f in ("dv_paged_proj.cuh", "dv_paged.cu"))
+    held = int(re.search(r"constexpr int PQ_MAX_TILES = (\d+);", proj).group(1))
+    most = re.search(r"qkv_most_tiles\(.*?\{\s*return (.*?);", proj, re.S).group(1)
+    for src, py in (("3ll", "3"), ("2ll", "2"), ("(all ? 2 * h : 0)", "2 * h"), ("dh / 8", "dh // 8")):
+        most = most.replace(src, py)
+    most_tiles = eval(most, dict(kh_max=1000, h=1024, dh=128))  # every entry invalid, exact_kv
+    assert most_tiles == (3 * 1000 + 2 * 1024) * 16
+    # CTA c has tiles floor(n c / 148) up to floor(n (c + 1) / 148)
+    assert max(most_tiles * (c + 1) // 148 - most_tiles * c // 148 for c in range(148)) <= -(-most_tiles // 148) <= held
+    assert "per_cta <= PQ_MAX_TILES" in host and "s_row[PQ_MAX_TILES]" in proj
