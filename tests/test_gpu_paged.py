@@ -607,6 +607,98 @@ def test_a_block_of_many_heads_whose_set_names_none(B, bad):
     assert torch.equal(out, c["bO"].expand(B, d))
 
 
+def check_block(c, out, exact=False, out0=None):
+    """The block's output and the rows that it stored against 64 bits.
+
+    A stored value is its sum rounded once: half a step of the pool's type (bf16 2^-8, fp32 2^-24), and the sum's error: fp32
+    chains of at most 64 steps, 2^-18 of the terms' magnitudes. The output is compared with the attention over what the pages
+    hold, and 64 chained steps of 2^-23 make 2^-17 of its norm, with the scores' and weights' 2^-16. From nine requests on, with
+    bf16 weights, y and the attention's result enter as two bf16 terms: each value off by 2^-18, independently, so q by
+    2^-18 of its norm, scores by 2^-18 |q| |k| scale <= 2^-15 here, weights by 2^-14, the output by less than 2^-13."""
+    two = c["K"].dtype == BF16 and c["y"].shape[0] > 8
+    sums, mags = block_sums(c)
+    half = 2.0 ** -8 if c["K"].dtype == BF16 else 2.0 ** -24
+    n = c["K"].shape[0] * c["page"]
+    for b, sl in enumerate(c["slots"].tolist()):
+        if not 0 <= sl < n:
+            continue
+        p, o = divmod(sl, c["page"])
+        for i in range(c["K"].shape[1]):
+            for pool, m in (("K", 1), ("V", 2)):
+                got = c[pool][p, i, o].double()
+                if not exact and i not in c["heads"]:
+                    assert not got.any()
+                else:
+                    ref, mag = sums[b, i, m], mags[b, i, m]
+                    assert ((got - ref).abs() <= ref.abs() * half + mag * (2.0 ** -17 if two else 2.0 ** -18)).all()
+    ref = block_out(c, sums[:, :, 0])
+    got = out.double() - (0 if out0 is None else out0.double())
+    err = (got - ref).norm() - (0 if out0 is None else 2.0 ** -24 * out.double().norm())  # (one fp32 addition more)
+    assert err <= (2.0 ** -13 if two else 2.0 ** -16) * ref.norm()
+
+
+KINDS = [(BF16, 1), (BF16, 4), (BF16, 8), (BF16, 9), (BF16, 13), (BF16, 16), (F32, 1), (F32, 4), (F32, 16)]
+
+
+def kind_case(dtype, B, heads, seed=0, top=60):
+    return block_case(B, 512, 6, 64, heads, [(23 * (b + 1)) % top + (b != 2) for b in range(B)], 10 * B + seed, dtype=dtype)
+
+
+@pytest.mark.parametrize("exact, acc", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("dtype, B", KINDS)
+def test_a_block_in_every_form(dtype, B, exact, acc):
+    c = kind_case(dtype, B, [0, 2, 3, 5])
+    out0 = torch.randn(B, 512, generator=gen(4), device="cuda")
+    for _ in range(2):
+        out, status = run_block(c, exact=exact, accumulate=acc, out=out0.clone())
+        assert status == 0
+        check_block(c, out, exact=exact, out0=out0 if acc else None)
+
+
+@pytest.mark.parametrize("exact", [False, True])
+@pytest.mark.parametrize("dtype, B", KINDS)
+def test_a_block_skips_and_flags_what_is_out_of_range(dtype, B, exact):
+    # heads out of range between valid ones: as without them
+    c = kind_case(dtype, B, [1, 4], 1)
+    out, status = run_block(c, exact=exact, idx=[-1, 1, 6, 4, 2 ** 31 - 1], kh=5)
+    assert status == bd.DV_DEV_INDEX_RANGE
+    check_block(c, out, exact=exact)
+    # a count above the bound, and below zero: clamped
+    c = kind_case(dtype, B, [0, 3], 2)
+    out, status = run_block(c, exact=exact, idx=[0, 3, 5], count=3, kh=2)
+    assert status == bd.DV_DEV_COUNT_CLAMPED
+    check_block(c, out, exact=exact)
+    c = kind_case(dtype, B, [], 3)
+    out, status = run_block(c, exact=exact, idx=[0, 3], count=-7)
+    assert status == bd.DV_DEV_COUNT_CLAMPED
+    check_block(c, out, exact=exact)
+    # a slot outside the pools, and a negative one: nothing is stored, the pages hold what they held
+    c = kind_case(dtype, B, [2, 5], 4)
+    c["slots"][0] = c["K"].shape[0] * c["page"]
+    if B > 1:
+        c["slots"][1] = -5
+    held = c["K"].clone(), c["V"].clone()
+    out, status = run_block(c, exact=exact)
+    assert status == bd.DV_DEV_INDEX_RANGE
+    check_block(c, out, exact=exact)
+    mine = torch.ones(c["K"].shape[0], c["page"], dtype=torch.bool, device="cuda")
+    for sl in c["slots"].tolist():
+        if 0 <= sl < mine.numel():
+            mine[sl // c["page"], sl % c["page"]] = False
+    for now, before in zip((c["K"], c["V"]), held):
+        same = (now == before) | (now.isnan() & before.isnan())
+        assert same.transpose(1, 2)[mine].all()
+    # a page out of range: its keys are left out; the new token's slot is another request's page, which stays whole
+    c = kind_case(dtype, B, [0, 1, 2], 5, 100)
+    c["lens"][0], c["slots"][0] = 20, -1
+    pages = c["table"][0].clone()
+    c["table"][0, 1] = c["K"].shape[0]
+    out, status = run_block(c, exact=exact)
+    assert status == bd.DV_DEV_INDEX_RANGE
+    c["table"][0, 1], c["lens"][0] = pages[2], 12  # the keys of pages 0 and 2
+    check_block(c, out, exact=exact)
+
+
 def test_a_block_captured_and_replayed_follows_its_inputs():
     """One captured dv_sparse_mha_paged, replayed after the lengths, slots, set and input changed in place."""
     d, h, dh, page, B = 512, 6, 64, 8, 3
