@@ -289,7 +289,10 @@ __global__ void __launch_bounds__(PS_THREADS)
 // element. A thread moves eight channels of K and of V; 16384 tokens of 32 heads
 // of 128 channels into bf16 pages take 137 us, 0.89 of the copy bandwidth. Two
 // or four such pieces a thread were slower (155, 146 us), evict-first loads too
-// (150 us).
+// (150 us), and loads past the L1 cache (169 us: a warp's two 16-byte loads of k
+// share their sectors). The loads are coherent, since the kernel before may
+// still be writing k and v when this one becomes resident; read-only ones took
+// the same time.
 // ----------------------------------------------------------------------------
 constexpr int PA_THREADS = 256;
 
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_append_kernel(PagedAppendArg
   }
   const float4* ks = reinterpret_cast<const float4*>(a.k) + 2ll * i;
   const float4* vs = reinterpret_cast<const float4*>(a.v) + 2ll * i;
-  const float4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+  const float4 k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
   const int p = slot / a.page;
   const long long row = (long long)p * a.stride_rows + head * a.page + (slot - p * a.page);
   store8<KT>(static_cast<KT*>(a.K) + (row * a.dh8 + c) * 8, k0, k1);

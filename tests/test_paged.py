@@ -178,3 +178,12 @@ def test_the_projections_tile_list_holds_every_set():
     # CTA c has tiles floor(n c / 148) up to floor(n (c + 1) / 148)
     assert max(most_tiles * (c + 1) // 148 - most_tiles * c // 148 for c in range(148)) <= -(-most_tiles // 148) <= held
     assert "per_cta <= PQ_MAX_TILES" in host and "s_row[PQ_MAX_TILES]" in proj
+
+
+def test_paged_kernels_take_no_read_only_loads():
+    """A kernel launched with programmatic serialisation may be resident while the kernel before it still writes its inputs, so
+    they are read by coherent loads: the read-only path asks for data that does not change while the kernel lives."""
+    here = os.path.join(os.path.dirname(bd.__file__), "csrc")
+    for f in ("dv_paged.cuh", "dv_paged_proj.cuh", "dv_paged.cu"):
+        code = re.sub(r"//[^\n]*", "", open(os.path.join(here, f)).read())
+        assert not re.search(r"__ldg\s*\(|ld\.global[.\w:]*\.nc", code), f
