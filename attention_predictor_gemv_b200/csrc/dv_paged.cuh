@@ -156,8 +156,9 @@ __global__ void __launch_bounds__(PT_THREADS) page_tables_kernel(PageTablesArgs 
     sum = {sum.gone + tot.gone, sum.need + tot.need, sum.add + tot.add};
   }
   const int F = (int)sum.gone;
-  const int avail = min(fc + F, a.n_pages);
-  if (fc + F > a.n_pages) bad |= ST_RANGE;
+  // (a free count that does not go with the lengths: the sum is above n_pages, and may pass 31 bits)
+  const int avail = (int)min((unsigned)fc + (unsigned)F, (unsigned)a.n_pages);
+  if (F > a.n_pages - fc) bad |= ST_RANGE;
   unsigned need_ok = sum.need, tok_ok = sum.add;
   if (__syncthreads_and(all_fit) && sum.need <= (unsigned)avail && sum.add <= (unsigned)a.T) {
     if (cluster_rank() == 0)
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(PT_THREADS) page_tables_kernel(PageTablesArgs 
     const int r = row_of(s_free, R, i);
     const int oldp = (s_len[r] + a.page - 1) / a.page;
     const int newp = oldp - (s_free[r + 1] - s_free[r]);
-    if (fc + i < a.n_pages) a.free_list[fc + i] = a.table[(size_t)r * a.W + newp + (i - s_free[r])];
+    if (i < a.n_pages - fc) a.free_list[fc + i] = a.table[(size_t)r * a.W + newp + (i - s_free[r])];
   }
   cluster_barrier();  // every CTA has read lens and want; the pushes are visible
   for (int i = gt; i < (int)need_ok; i += GT) {

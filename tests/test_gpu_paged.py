@@ -362,6 +362,20 @@ def test_page_tables_flag_what_is_not_a_length_or_a_count():
     assert got["table"][2] == [4, 6] and got["slots"] == [12] + [-1] * 7 and got["free_count"] == 1
 
 
+@pytest.mark.parametrize("n_pages, count", [(12, 12), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_page_tables_clamp_a_free_count_that_leaves_no_room(n_pages, count):
+    """More free pages than the stack holds once pages come back: flagged, nothing is pushed behind its end."""
+    stack = torch.full((n_pages,), 5, dtype=torch.int32, device="cuda")
+    table, free = i32([[1, 2], [-1, -1]]), i32([count])
+    slots, offsets, granted, lens = i32([9, 9]), i32([9] * 3), i32([9, 9]), i32([2, 0])
+    ws = bd.workspace(bd.DV_OP_PAGE_TABLES, bd.dims())
+    bd.dv_page_tables(i32([0, 1]), lens, lens, table, stack, free, free, slots, offsets, granted, 1, ws)
+    assert bd.dv_read_device_status(ws) == bd.DV_DEV_INDEX_RANGE
+    assert lens.tolist() == [0, 1] and granted.tolist() == [1, 1] and offsets.tolist() == [0, 0, 1]
+    assert free.item() == n_pages - 1 and table.tolist() == [[1, 2], [5, -1]] and slots.tolist() == [5, -1]
+    assert (stack[:: max(1, n_pages // 1000)] == 5).all() and (stack[-8:] == 5).all()
+
+
 def test_page_tables_repeat_from_the_same_lengths():
     m = random_tables(40, 5, 8, 3, 0.6)
     a = run_tables(m, 500)[0]
