@@ -975,7 +975,7 @@ dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, co
   if ((dh != 64 && dh != 128) || h > KV_REST_MAX_H) return DV_ERR_UNSUPPORTED;
   dv_dims D = {B, d, 1, 0, h, dh, 0, 0, kh_max};
   if (!dims_ok(D)) return DV_ERR_ARG;
-  if (kv->page > (INT32_MAX - 32) / W || ((long long)W * kv->page + 16) / 16 * B > INT32_MAX / h) return DV_ERR_UNSUPPORTED;
+  if (kv->page > (INT32_MAX - 32) / W || !paged_units_ok(kv, B, W, h, 1)) return DV_ERR_UNSUPPORTED;
   const PagedLayout P = paged_layout(D, wbytes_of(wdtype));
   const Layout& L = P.L;
   if (!ok_ptr(ws)) return ws ? DV_ERR_ALIGN : DV_ERR_ARG;

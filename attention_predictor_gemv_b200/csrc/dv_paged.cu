@@ -68,6 +68,11 @@ dv_status paged_kv_check(const dv_paged_kv* kv) {
   return DV_OK;
 }
 
+bool paged_units_ok(const dv_paged_kv* kv, int B, int W, int rows, int G) {
+  // the units of all requests and heads are numbered with 31 bits, and rounded up to the warps of all CTAs
+  return ((long long)W * kv->page + 16) / 16 * B * ((G + 7) / 8) <= (INT32_MAX - PAGED_UNITS_SPARE) / rows;
+}
+
 cudaError_t run_paged_attn(const dv_paged_kv* kv, const float* q, int B, int rows, int G, const int32_t* table, int W,
                            const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
                            float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st, bool early) {
@@ -292,8 +297,7 @@ dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, c
     if (!ok_opt(p)) return DV_ERR_ALIGN;
   if (B > PAGED_MAX_ROWS || kv->page > (INT32_MAX - 32) / W || h_q > INT32_MAX / kv->dh) return DV_ERR_UNSUPPORTED;
   const int rows = head_idx ? kh_max : kv->h_kv, G = h_q / kv->h_kv;
-  // the units of all requests and heads are numbered with 31 bits
-  if (((long long)W * kv->page + 16) / 16 * B * ((G + 7) / 8) > INT32_MAX / (rows > 0 ? rows : 1)) return DV_ERR_UNSUPPORTED;
+  if (!paged_units_ok(kv, B, W, rows > 0 ? rows : 1, G)) return DV_ERR_UNSUPPORTED;
   s = ws_check(ws, ws_bytes, WS_HEADER + 4 * paged_attn_part_floats(kv->dh));
   if (s != DV_OK) return s;
   if (head_idx && kh_max == 0) return DV_OK;

@@ -13,6 +13,7 @@ constexpr size_t WS_HEADER = 72 * 1024;    // every workspace's fixed header (st
 constexpr size_t WS_TICKETS = 1024;        // offset of the attention counters in it
 constexpr int PAGED_MAX_ROWS = 4096;       // requests of a call, at most
 constexpr int PAGED_MAX_DH = 256;
+constexpr int PAGED_UNITS_SPARE = 8192;    // more than the warps of a launch
 
 struct PagedAttnArgs {
   const float* q;             // [B][rows][G][dh]
@@ -35,6 +36,8 @@ struct PagedAttnArgs {
 size_t paged_attn_part_floats(int dh);
 // Whether the pool's sizes are within what the kernels index with; DV_OK or the error.
 dv_status paged_kv_check(const dv_paged_kv* kv);
+// Whether the attention's work on B requests of up to W pages can be numbered.
+bool paged_units_ok(const dv_paged_kv* kv, int B, int W, int rows, int G);
 cudaError_t run_paged_attn(const dv_paged_kv* kv, const float* q, int B, int rows, int G, const int32_t* table, int W,
                            const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
                            float* out, float* lse, float* part, unsigned* tick, int* status, cudaStream_t st, bool early = false);

@@ -504,9 +504,9 @@ DV_API dv_status dv_paged_append(const dv_paged_kv* kv, const float* k, const fl
  * without dh), entry j belonging to head head_idx[j]; entries from the count
  * on are left as they were. Slots past a request's length are never used,
  * whatever they hold. A page or head index out of range leaves its keys
- * out and is flagged (DV_DEV_INDEX_RANGE). B * (W * page / 16) * heads read,
- * times h_q / h_kv / 8 rounded up, must be below 2^31 (DV_ERR_UNSUPPORTED). Finite q, K and V are assumed
- * where they are used; results do not depend on the order in which CTAs end. */
+ * out and is flagged (DV_DEV_INDEX_RANGE). B * (W * page / 16 + 1) * heads read,
+ * times h_q / h_kv / 8 rounded up, must be below 2^31 - 8192 (DV_ERR_UNSUPPORTED). Finite q, K
+ * and V are assumed where they are used; results do not depend on the order in which CTAs end. */
 DV_API dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int h_q, const int32_t* table, int W,
                                const int32_t* lens, float scale, const int32_t* head_idx, const int32_t* head_count,
                                int kh_max, float* out, float* lse, void* ws, size_t ws_bytes, dv_stream_t stream);

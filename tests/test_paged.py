@@ -187,3 +187,12 @@ def test_paged_kernels_take_no_read_only_loads():
     for f in ("dv_paged.cuh", "dv_paged_proj.cuh", "dv_paged.cu"):
         code = re.sub(r"//[^\n]*", "", open(os.path.join(here, f)).read())
         assert not re.search(r"__ldg\s*\(|ld\.global[.\w:]*\.nc", code), f
+
+
+def test_attn_units_leave_room_for_rounding_up():
+    """The units are rounded up to the warps of all CTAs in 31 bits: at most 8 warps of 2 CTAs on 148 SMs, under 8192."""
+    wide = _kv(h_kv=64)
+    assert _attn(wide, h_q=64, W=2 ** 25 - 2, wsb=16) == bd.DV_ERR_UNSUPPORTED  # 2^31 - 64 units
+    assert _attn(wide, h_q=64, W=2 ** 25 - 2 - 128, wsb=16) == bd.DV_ERR_WORKSPACE  # 2^31 - 64 - 8192: past this check
+    assert _mha(_kv(h_kv=64), W=2 ** 25 - 2) == bd.DV_ERR_UNSUPPORTED
+    assert _mha(_kv(h_kv=64), W=2 ** 25 - 2 - 128, wsb=1 << 16) == bd.DV_ERR_WORKSPACE
