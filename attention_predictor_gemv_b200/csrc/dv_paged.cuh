@@ -427,17 +427,18 @@ __global__ void __launch_bounds__(PA_THREADS) paged_token_kernel(PagedTokenArgs 
 // fragments' 16-byte reads have no bank conflicts); K of the next unit is
 // requested once the scores of this one are formed, its V once this one's is
 // used, the next item's q with it. No barrier in the loop. Any page size and
-// alignment of pages costs the same (54.5 us with pages of 16, 55.0 with 8).
+// alignment of pages costs the same (55 us with pages of 16 and of 8).
 // Measured on the way: fragments loaded from global memory directly 71 us
 // (8 rows of 64 bytes a load hold the L1 path at 4.8 TB/s), row-wise bulk copies
 // 4.3 TB/s in a copy test that ran 6.3 TB/s with these; 4 warps in two CTAs the
 // same; three CTAs' worth of shorter stretches per SM slower (66 us).
 //
 // Bound by HBM for long contexts: 16 requests of 32 heads, 0 to 2176 keys,
-// 54.5 us (5.2 TB/s, 0.80 of the copy bandwidth); 64 requests of 64 heads over
-// 8, 0 to 8192 keys, 190 us (5.7 TB/s, 0.86); one of 131071 keys 98 us (0.83).
-// About 8 us of each are launch, schedule, the first rows' latency and the
-// joins; SMs finish up to 15 % apart. One request of 65 keys: 6.6 us.
+// 55 us on the device (5.2 TB/s, 0.79 of the copy bandwidth); 64 requests of 64
+// heads over 8, 0 to 8192 keys, 193 us (5.6 TB/s, 0.85); one of 131071 keys
+// 98 us (0.84). About 8 us of each are launch, schedule, the first rows' latency
+// and the joins; the last SM's loop ends 18 % after the median one's. One
+// request of 65 keys: 6.5 us.
 // ----------------------------------------------------------------------------
 constexpr int PGA_JOIN = 16;  // CTAs' partials that one CTA adds, at most (of more, groups first)
 
@@ -554,7 +555,10 @@ __global__ void __launch_bounds__(32 * PagedShape<KT, NB, QR>::WARPS, PagedShape
   }
   const int HR = a.rows * a.G;  // query rows of a request
   int units = 0, same = 0;  // units of all rows; of each where they are equal
-  if (a.B <= 32) {  // every warp for itself, the same values: no barrier
+  // Up to 32 rows: every warp for itself, the same values, no barrier, and rows of one length are seen at once. More go by
+  // the even share, whose items may cross CTAs: 33 rows of 65 keys of 32 heads 17.1 us, 32 rows 15.3 us; 55.4 and 53.8 us
+  // with 520 keys, and no difference a row with 2048.
+  if (a.B <= 32) {
     const int len = lane < a.B ? a.lens[lane] : 0;
     if (len > cap && blockIdx.x == 0 && warp == 0) raise_status(a.status, ST_CLAMPED);
     units = len > 0 ? (min(len, cap) + UNIT - 1) / UNIT : 0;

@@ -31,7 +31,7 @@ template <bool ONE>
 __device__ __forceinline__ void a_words(float x, float y, int g, uint32_t& a_top, uint32_t& a_low, uint32_t& b_low) {
   uint32_t h, m, l;
   split3(x, y, h, m, l);
-  // (masks, not choices: those became branches, and the q, k, v kernel took 60 us for 36)
+  // (masks: choices by row became branches)
   const uint32_t row0 = g == 0 ? ~0u : 0u, row1 = g == 1 ? ~0u : 0u;
   a_top = ONE ? (h & row0) | (l & row1) : h;
   a_low = ONE ? m & row0 : m;
@@ -45,10 +45,11 @@ __device__ __forceinline__ void a_words(float x, float y, int g, uint32_t& a_top
 // memory, since loads of it within the loop queue behind the weights in flight.
 // k and v are rounded into slots[b]; without `all` the places of the other heads
 // are cleared. Two forms, below.
-// 5376 rows of 12288 channels (132 MB), one request: 31 us under a profiler,
-// 4.3 TB/s; 7680 rows of 4096 channels (63 MB), four requests: 20 us. Bound by
+// 5376 rows of 12288 channels (132 MB), one request: 34 us under a profiler,
+// 3.9 TB/s; 7680 rows of 4096 channels (63 MB), four requests: 22 us. Bound by
 // the 4 us before the first rows arrive, by CTAs of five tiles where the mean is
-// 4.5, and with more requests by the loop's instructions.
+// 4.5, by the rows read once more (below, 2 us), and with more requests by the
+// loop's instructions.
 // ----------------------------------------------------------------------------
 struct PagedQkvArgs {
   const __nv_bfloat16* W;
@@ -130,10 +131,11 @@ __device__ __forceinline__ QkvTile qkv_tile(const PagedQkvArgs& a, int nsel, con
 // partial sums, added, are 2.3 times that spread for independent terms, but no more than the value itself where one warp
 // has all channels, so the largest of the 32 values that a warp stores is taken: 2 to 4 times the spread, and 2^-22 of it
 // 4 to 7 times the error (fewer channels have smaller errors).
-// About one value in 400 is formed again, by the whole CTA at its end, about 2 us each where 12288 channels: four requests
-// of 4096 channels 48.5 us a call for 46 without it, one of 12288 channels 53.5 us for 52. By a warp each, at once, these
-// took 53 and 64 us; with the rows' loads through shared memory, all at once, the same; with the loop unrolled by three
-// the first took a microsecond more.
+// About one value in 500 is formed again, by the whole CTA at its end: 2500 cycles each of 4096 channels and 8000 of 12288,
+// nearly all of them the loads while other SMs stream. A call with one request of 4096 channels takes 39 us with it and
+// 38 without, with four 48.5 for 46, with eight 63 for 60; one request of 12288 channels 53.5 for 52, eight 103 for 96. By
+// a warp each, at once, four requests took 53 us and one of 12288 channels 64; the loads through shared memory, all at
+// once, the same as this; the loop unrolled by three or six up to 1.5 us more with 4096 channels.
 constexpr int QC_ENTRIES = PP_THREADS + 128, QC_ROUND = 32;
 struct QkvClose {
   long long to[QC_ENTRIES];  // the value's element of its pool, doubled, odd: of V
@@ -258,8 +260,9 @@ __host__ __device__ constexpr long long qkv_most_tiles(int kh_max, int h, int dh
 constexpr int PQ_MAX_TILES = 576;  // of a CTA; more on an SM: refused on the host. 1000 entries, 1024 heads of 128 on 148 SMs: 546
 
 // One request: a tile of 8 rows at a time, 512 channels of each row a warp and ring slot, so that what lies together in
-// memory is read together; y's terms, formed once, come from shared memory. For up to 12288 channels: 31 us at the
-// larger size above, where the other form took 34 us.
+// memory is read together; y's terms, formed once, come from shared memory, and limit it to 12288 channels. Whole calls
+// with 512, 2048, 4096, 8192 and 12288 channels: 15.2, 19.6, 37.1, 46.0 and 54.3 us; by the other form 15.6, 20.2, 38.5,
+// 48.5 and 60.3.
 constexpr int PT_CW = 512, PT_PITCH = 2 * PT_CW + 16, PT_SLOT = 8 * PT_PITCH, PT_SLOTS = 2, PT_MAX_D = 12288;
 constexpr int PT_HOLD = 8;  // tiles whose sums are kept before the warps' are added
 constexpr int PT_RING = PP_WARPS * PT_SLOTS * PT_SLOT, PT_RED = PT_HOLD * PP_WARPS * 8 * 4;
@@ -384,8 +387,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) paged_qkv_one_kernel(PagedQkvAr
 }
 
 // More requests (or channels): they are the rows; a slot holds four tiles of 128 channels, and y's terms are formed once
-// for them, from y in shared memory (a segment of the channels at a time where it is larger than 64 KB). The form above
-// took 25 us for 20 us at four requests; slots of 64 channels of eight tiles, or 16 warps, the same time.
+// for them, from y in shared memory (a segment of the channels at a time where it is larger than 64 KB). With four
+// requests of 4096 channels the form above took 25 us where this took 20; slots of 64 channels of eight tiles, or 16
+// warps, the same time.
 constexpr int PQ_TILES = 4, PQ_SLOTS = 2, PQ_PITCH = 256 + 16;
 constexpr int PQ_SLOT = PQ_TILES * 8 * PQ_PITCH;
 constexpr int PQ_STRIDE = 128 * PP_WARPS;                // channels that the warps take side by side

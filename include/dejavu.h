@@ -513,19 +513,24 @@ DV_API dv_status dv_paged_attn(const dv_paged_kv* kv, const float* q, int B, int
 
 /* dv_sparse_mha over a paged cache, every batch row with its own length: for
  * the heads in head_idx, q, k, v of the new token are computed, k and v are
- * stored in slots[b] (from dv_page_tables; negative: not stored), the
- * attention runs over lens[b] tokens (the new one included), and
+ * stored in slots[b] (negative: not stored), the attention runs over lens[b]
+ * tokens (the new one included), and
  *   out[b] (+)= sum_{i in S_A} H_i WOt[i] (+ bO).
  * y, Wqkv, bqkv, WOt, bO, head_idx, head_count, kh_max, out, accumulate as
  * for dv_sparse_mha (h = kv->h_kv heads, dh 64 or 128, kv->kvdtype = wdtype,
- * h <= 1024). exact_kv nonzero: k and v of the unselected heads are computed
- * and stored too; 0: their place in slots[b] is set to zero, since a recycled page
+ * h <= 1024). slots has one entry per row, where dv_page_tables gives the slots
+ * of all added tokens in a row: of row b they start at slots[offsets[b]], and it
+ * has none where offsets[b + 1] = offsets[b].
+ * exact_kv nonzero: k and v of the unselected heads are computed and stored too; 0: their place in slots[b] is set to zero, since a recycled page
  * holds another request's keys and values. A row of length 0 gets bO alone.
  * The attention reads k and v of the new token as they are stored. Where few
  * keys are attended to, one bf16 step of one of them moves out by up to 2e-4 of
  * its norm, so with bf16 weights and B <= 8 they are the exact sums, rounded to
  * fp32 and then to bf16, for any B and set; sums in another order (a plain fp32
- * matrix product's, the contiguous call's) may store a neighbouring value. */
+ * matrix product's, the contiguous call's) may store a neighbouring value. From
+ * B = 9 on bf16 weights are multiplied with y and the attention's result in two
+ * bf16 terms, as in dv_sparse_mha: each value is off by up to 2^-18 of itself,
+ * and k and v may be a neighbouring value too. */
 DV_API dv_status dv_sparse_mha_paged(const float* y, int B, int d, const void* Wqkv, const float* bqkv,
                                      const void* WOt, const float* bO, dv_dtype wdtype, const dv_paged_kv* kv,
                                      const int32_t* table, int W, const int32_t* lens, const int32_t* slots,
