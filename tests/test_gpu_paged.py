@@ -713,6 +713,43 @@ def test_a_block_skips_and_flags_what_is_out_of_range(dtype, B, exact):
     check_block(c, out, exact=exact)
 
 
+@pytest.mark.parametrize("dtype, B", [(BF16, 1), (BF16, 5), (BF16, 12), (F32, 3)])
+def test_blocks_on_two_streams_and_in_two_graphs(dtype, B):
+    """Two layers' blocks at once, each with its own workspace: eager on two streams, then two graphs replayed on them."""
+    cs = [kind_case(dtype, B, [0, 2, 3], 7 + i) for i in range(2)]
+    want = [run_block(c)[0] for c in cs]
+    # fp32 weights add their partial sums by float atomics: at most 3 * 64 terms in any order, 2^-24 each of a partial sum
+    near = lambda a, b: torch.equal(a, b) if dtype == BF16 else (a - b).norm() <= 192 * 2.0 ** -24 * 192 ** 0.5 * b.norm()  # noqa: E731
+    wss = [bd.workspace(bd.DV_OP_SPARSE_MHA_PAGED, bd.dims(B=B, d=512, h=6, dh=64, kh_max=3)) for _ in cs]
+    kvs, outs = [bd.PagedKV(c["K"], c["V"]) for c in cs], [torch.empty(B, 512, device="cuda") for _ in cs]
+    idx, cnt = i32([0, 2, 3]), i32([3])
+    streams, graphs = [torch.cuda.Stream() for _ in cs], [torch.cuda.CUDAGraph() for _ in cs]
+
+    def call(i, stream=None):
+        c = cs[i]
+        bd.dv_sparse_mha_paged(c["y"], c["Wqkv"], c["bqkv"], c["WOt"], c["bO"], kvs[i], c["table"], c["lens"], c["slots"], 0.125, idx, cnt, 3,
+                               outs[i], wss[i], stream=stream)
+
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            call(i, s)
+    torch.cuda.synchronize()
+    assert all(near(a, b) for a, b in zip(outs, want))
+    for i, s in enumerate(streams):
+        with torch.cuda.graph(graphs[i], stream=s):
+            for _ in range(3):
+                call(i)
+        outs[i].fill_(9.0)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(near(a, b) for a, b in zip(outs, want)) and all(bd.dv_read_device_status(ws) == 0 for ws in wss)
+
+
 def test_a_block_captured_and_replayed_follows_its_inputs():
     """One captured dv_sparse_mha_paged, replayed after the lengths, slots, set and input changed in place."""
     d, h, dh, page, B = 512, 6, 64, 8, 3
